@@ -364,9 +364,9 @@ def work(c):
         add = _lens(c["lens_seed"] + 1, c["B"], c["add_lo"], c["add_hi"])
         held = sum(_blocks(x, c["bs"]) for x in lens)
         fresh = sum(_blocks(x + a, c["bs"]) for x, a in zip(lens, add)) - held
-        # lengths, counts, held entries (checked) and popped ids read; new
-        # entries, lengths, offsets and slots written
-        return dict(bytes=16 * c["B"] + 4 * held + 8 * fresh + 8 * (sum(add) + c["pad"]), flops=0)
+        # lengths, counts, the entry of each sequence's last block and popped
+        # ids read; new entries, lengths, offsets and slots written
+        return dict(bytes=20 * c["B"] + 8 * fresh + 8 * (sum(add) + c["pad"]), flops=0)
     if c["kind"] == "store":
         return dict(bytes=c["T"] * (8 * c["heads"] * c["dim"] + 8), flops=0)
     Hq, Hkv, D = c["q_heads"], c["kv_heads"], c["dim"]
