@@ -78,7 +78,8 @@ typedef enum {
                             set to -1 and the others are still computed      */
 } spec_status;
 
-typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
+/* Logits are SPEC_F32 or SPEC_BF16; attention takes SPEC_BF16 or SPEC_F16. */
+typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1, SPEC_F16 = 2 } spec_dtype;
 
 /* Limits checked on the host. */
 #define SPEC_MAX_K 256           /* drafts per sequence per call      */
@@ -86,6 +87,8 @@ typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
 #define SPEC_MAX_V (1 << 21)     /* vocabulary size                   */
 #define SPEC_MAX_COMMIT_B 16384  /* sequences per paged commit        */
 #define SPEC_MAX_FUSED_B 4096    /* sequences per fused verify+commit */
+#define SPEC_MAX_CONTEXT (1 << 30) /* positions a block table can cover; packed rows */
+#define SPEC_MAX_HEAD_DIM 128    /* columns of a head in attention    */
 #define SPEC_MAX_CACHED 1024     /* cached tokens per sequence (Saguaro) */
 #define SPEC_VP_MAX_RANKS 64     /* vocabulary shards (ranks)         */
 #define SPEC_VP_ROW_BYTES 32     /* one row record of a shard         */
@@ -245,6 +248,132 @@ int spec_commit_paged(int B, int block_size, int max_blocks,
                       void* kv_pool, int layers, int kv_heads, int head_dim,
                       const void* hid_stage, void* hid_out, int32_t* hid_off,
                       int hidden, int32_t* dev_status, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Growing block tables, with the slots of the new rows ([HS] Unterstuetzung
+ * fuer Batch-Inferenz: paged attention with block tables, every sequence its
+ * own length). The step before rows enter the cache: a request is admitted
+ * (length 0, its prompt's length added), a prompt is taken in chunks, or a
+ * decoding step adds its rows. (spec_commit_paged grows tables too, by rows it
+ * copies from the staging buffer; freeing is its job: base_len 0, keep 0.)
+ *
+ * block_tables : in/out int32 [B, max_blocks], as for spec_commit_paged.
+ * seq_lens, add_len : int32 [B]: the lengths and the rows each sequence gains
+ *         (0: none).
+ * free_stack (int32 [num_blocks]), free_top (device int32): read only. Missing
+ *         blocks are popped from the top, sequences ascending, entries
+ *         ascending, as by spec_commit_paged.
+ * new_lens, new_top : out int32 [B], device int32: the lengths and the stack
+ *         height afterwards; may be seq_lens and free_top themselves.
+ * row_off : out int32 [B+1], exclusive scan of add_len: the packed row where
+ *         each sequence's new rows start.
+ * slot_map : optional out int64 [capacity] (NULL to skip): entry row_off[b] + i
+ *         is the slot block * block_size + offset of the i-th new row of
+ *         sequence b; entries from row_off[B] on are -1, so a captured graph
+ *         may use one capacity for batches of any size.
+ * Every check (lengths and counts not negative, new lengths within the table,
+ * the entry of a part-filled last block and popped ids inside
+ * [0, num_blocks), the stack's height, row_off[B] <= capacity) is made before
+ * anything is written; on failure *dev_status (required) gets SPEC_EINVAL or
+ * SPEC_ENOBLOCKS and nothing else is changed. Does nothing while *dev_status
+ * holds an error.
+ * ------------------------------------------------------------------------- */
+int spec_extend_paged(int B, int block_size, int max_blocks, int32_t* block_tables,
+                      const int32_t* seq_lens, const int32_t* add_len,
+                      const int32_t* free_stack, const int32_t* free_top, int num_blocks,
+                      int32_t* new_lens, int32_t* new_top, int32_t* row_off,
+                      int64_t* slot_map, int64_t capacity, int32_t* dev_status, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Storing K/V rows of one layer in the paged pool ([HS] Unterstuetzung fuer
+ * Batch-Inferenz). For rows that need no check first, such as a prompt's; rows
+ * that a check may drop are staged and stored by the commit.
+ *
+ * k, v     : rows of 2-byte elements [T, kv_heads, head_dim], heads contiguous;
+ *            row t starts at element t * ld_k / t * ld_v (so k and v may be
+ *            parts of one projection's output). Rows start on 16-byte
+ *            boundaries; kv_heads * head_dim * 2 is a multiple of 16.
+ * slot_map : int64 [T], as written by spec_extend_paged; rows with slot -1 are
+ *            skipped. Any other slot outside [0, num_blocks * block_size)
+ *            records SPEC_EINVAL and its row is skipped. Of rows that name the
+ *            same slot any one may end up there, or parts of several.
+ * kv_pool  : [num_blocks, layers, 2, block_size, kv_heads, head_dim], as for
+ *            spec_commit_paged; `layer` is the layer written.
+ * Does nothing while *dev_status (may be NULL) holds an error.
+ * ------------------------------------------------------------------------- */
+int spec_store_kv(const void* k, int64_t ld_k, const void* v, int64_t ld_v, int T,
+                  const int64_t* slot_map, void* kv_pool, int num_blocks, int layers, int layer,
+                  int block_size, int kv_heads, int head_dim, int32_t* dev_status,
+                  void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention of whole prompts, packed, causal, with grouped heads. (The pages
+ * name the exits' forward passes; this is the attention of one layer of them.)
+ *
+ * Sequence b has rows row_off[b] .. row_off[b+1]-1 of q, k, v and out. Row i
+ * of a sequence sees its rows 0..i:
+ *   out_i = sum_{j<=i} p_ij v_j,  p_ij = softmax_j(scale * q_i . k_j),
+ * query head h with K/V head h / (q_heads / kv_heads).
+ *
+ * q, out : [T, q_heads, head_dim], k, v : [T, kv_heads, head_dim], heads
+ *          contiguous, row t at element t * ld; 16-byte boundaries.
+ * dtype  : SPEC_BF16 or SPEC_F16 (all four). Products and sums are taken in
+ *          float32; the softmax weights are rounded to dtype for the product
+ *          with v.
+ * row_off: int32 [B+1], not decreasing, within [0, T]. A sequence whose range
+ *          is not is left out (SPEC_EDEVICE). Rows outside every range are
+ *          neither read nor written.
+ * q_heads: a multiple of kv_heads, at most 128 times it.
+ * head_dim: a multiple of 8, at most SPEC_MAX_HEAD_DIM.
+ * scale  : finite, > 0 (usually 1/sqrt(head_dim)).
+ * lse    : optional out float [T, q_heads] (NULL to skip): natural log of
+ *          sum_j exp(scale * q_i . k_j).
+ * dev_status : may be NULL. SPEC_ETIMEOUT if a bounded wait ran out (outputs
+ *          are then not to be used).
+ * ws     : spec_attend_workspace_bytes(head_dim) bytes, 256-byte aligned. No
+ *          initial contents are needed. Calls that may overlap on the GPU
+ *          (two graphs, two streams) need one each.
+ * Where v is not finite, rows that see it get what the sum gives; so may rows
+ * up to 127 keys earlier in the same sequence (a weight of 0 times it). What
+ * lies past a sequence's end never reaches it.
+ * ------------------------------------------------------------------------- */
+size_t spec_attend_workspace_bytes(int head_dim);
+int spec_attend_prompt(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
+                       int64_t ld_v, int dtype, const int32_t* row_off, int B, int T,
+                       int q_heads, int kv_heads, int head_dim, float scale, void* out,
+                       int64_t ld_out, float* lse, int32_t* dev_status, void* ws,
+                       size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention of new rows over the paged cache ([HS] paged attention with block
+ * tables; Wiederverwendung von KV-Cache: drafted rows' K/V stay staged until
+ * the check): one layer's attention for a decoding step (one row per
+ * sequence), for the K + 1 rows of a check, or for a chunk of a prompt.
+ *
+ * q, out, lse, dtype, scale, head sizes, ws, dev_status: as for
+ *          spec_attend_prompt.
+ * row_off: int32 [B+1] as there, or NULL: rows_per_seq rows for each
+ *          sequence (T = B * rows_per_seq).
+ * kv_pool, num_blocks, layers, layer, block_size, block_tables, max_blocks:
+ *          the pool and tables of spec_commit_paged; `layer` is the one read.
+ * seq_lens: int32 [B], positions in the cache.
+ * kv_stage: NULL: the new rows' K/V are in the cache already (seq_lens counts
+ *          them): row i of n sees positions 0 .. seq_lens-n+i. Else the
+ *          staging buffer of spec_commit_paged, [B, Kp1, layers, 2, kv_heads,
+ *          head_dim]: row i sees all seq_lens cached positions, then the
+ *          staged rows 0..i (n <= Kp1).
+ * A row that sees nothing gets out = 0 and lse = -infinity.
+ * A sequence with seq_lens negative or beyond the table, or more than Kp1 rows
+ * beside a staging buffer, sees nothing; a table entry outside
+ * [0, num_blocks) stands for rows of zeros; both record SPEC_EDEVICE.
+ * ------------------------------------------------------------------------- */
+int spec_attend_paged(const void* q, int64_t ld_q, int dtype, const int32_t* row_off,
+                      int rows_per_seq, int B, int T, int q_heads, const void* kv_pool,
+                      int num_blocks, int layers, int layer, int block_size, int kv_heads,
+                      int head_dim, const int32_t* block_tables, int max_blocks,
+                      const int32_t* seq_lens, const void* kv_stage, int Kp1, float scale,
+                      void* out, int64_t ld_out, float* lse, int32_t* dev_status, void* ws,
+                      size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Chain verification and the paged commit of its kept rows in one call

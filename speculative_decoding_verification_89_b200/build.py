@@ -8,14 +8,16 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libspecverify.so")
 SOURCES = ["row_stats.cu", "step.cu", "decide.cu", "draft.cu", "outcome.cu", "commit.cu",
-           "saguaro.cu", "vocab.cu", "capi.cu", "noalloc.cu"]
-HEADERS = ["common.cuh", "kernels.cuh", "draw.cuh", "commit.cuh", "rowmath.cuh"]
+           "saguaro.cu", "vocab.cu", "paged.cu", "attend.cu", "capi.cu", "noalloc.cu"]
+HEADERS = ["common.cuh", "kernels.cuh", "draw.cuh", "commit.cuh", "rowmath.cuh",
+           "paged.cuh", "attend.cuh", "attend_plan.cuh", "tc05.cuh"]
 
 NVCC_FLAGS = [
     "-std=c++17", "-O3", "-lineinfo",
@@ -45,15 +47,17 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     """Compile every source into ``libspecverify.so`` next to this file."""
     if not force and not _stale():
         return LIB
-    objs = []
+    objs, cmds = [], []
     for src in SOURCES:
         obj = os.path.join(CSRC, src.replace(".cu", ".o"))
-        cmd = [_nvcc(), *NVCC_FLAGS, *extra, "-I", os.path.join(ROOT, "include"),
-               "-c", os.path.join(CSRC, src), "-o", obj]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        subprocess.run(cmd, check=True)
+        cmds.append([_nvcc(), *NVCC_FLAGS, *extra, "-I", os.path.join(ROOT, "include"),
+                     "-c", os.path.join(CSRC, src), "-o", obj])
         objs.append(obj)
+        if verbose:
+            print(" ".join(cmds[-1]), flush=True)
+    # One compiler per core: the slowest sources take most of a minute each.
+    with ThreadPoolExecutor(os.cpu_count() or 1) as pool:
+        list(pool.map(lambda cmd: subprocess.run(cmd, check=True), cmds))
     tmp = LIB + ".tmp"
     cmd = [_nvcc(), "-shared", "-gencode", "arch=compute_100a,code=sm_100a",
            "-cudart", "static", "-o", tmp, *objs]

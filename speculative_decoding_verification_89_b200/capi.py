@@ -24,7 +24,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 SPEC_OK, SPEC_EINVAL, SPEC_ECUDA, SPEC_EWORKSPACE = 0, -1, -2, -3
 SPEC_ENOBLOCKS, SPEC_ETIMEOUT, SPEC_EDEVICE = -4, -5, -6
-SPEC_F32, SPEC_BF16 = 0, 1
+SPEC_F32, SPEC_BF16, SPEC_F16 = 0, 1, 2
 
 _p, _i, _i64, _u32, _u64, _sz = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
                                  ctypes.c_uint32, ctypes.c_uint64, ctypes.c_size_t)
@@ -54,6 +54,13 @@ _SIGS = {
                                                  _u64, _p, _u32, _p, _p, _p, _i, _i, _p, _p, _p,
                                                  _p, _p, _i, _p, _p, _i, _i, _i, _p, _p, _p, _i,
                                                  _p, _p, _sz, _p]),
+    "spec_extend_paged": (_i, [_i, _i, _i, _p, _p, _p, _p, _p, _i, _p, _p, _p, _p, _i64, _p, _p]),
+    "spec_store_kv": (_i, [_p, _i64, _p, _i64, _i, _p, _p, _i, _i, _i, _i, _i, _i, _p, _p]),
+    "spec_attend_workspace_bytes": (_sz, [_i]),
+    "spec_attend_prompt": (_i, [_p, _i64, _p, _i64, _p, _i64, _i, _p, _i, _i, _i, _i, _i,
+                                ctypes.c_float, _p, _i64, _p, _p, _p, _sz, _p]),
+    "spec_attend_paged": (_i, [_p, _i64, _i, _p, _i, _i, _i, _i, _p, _i, _i, _i, _i, _i, _i, _p,
+                               _i, _p, _p, _i, ctypes.c_float, _p, _i64, _p, _p, _p, _sz, _p]),
     "spec_philox_uniforms": (_i, [_u64, _p, _i, _p, _p]),
     "spec_last_cuda_error": (ctypes.c_char_p, []),
     "spec_verify_chain_noalloc": (_i, [_p, _i64, _p, _i64, _i, _i, _i, _i, _p, _p, _u64, _p,
@@ -293,6 +300,171 @@ def _kv_shapes(kv_stage, kv_pool, hid_stage, num_blocks, block_size):
     if hid_stage is not None:
         hidden = hid_stage.shape[-1]
     return layers, kv_heads, head_dim, hidden
+
+
+def _on_current_device(t):
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {t.device}, not on the current device")
+
+
+def _int_tensor(t, dtype, shape, name, like):
+    """t must be a contiguous tensor of this type and shape on like's device."""
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or \
+            t.device != like.device:
+        raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on {like.device}")
+
+
+def spec_extend_paged(block_tables, seq_lens, add_len, free_stack, free_top, new_lens, new_top,
+                      row_off, dev_status, block_size=16, slot_map=None, stream=None):
+    """Grow each sequence by add_len[b] rows: missing blocks into
+    block_tables, lengths and stack height into new_lens / new_top (which may
+    be seq_lens / free_top), packed row offsets into row_off int32 [B+1] and the
+    rows' pool slots into slot_map int64 [capacity]."""
+    B, max_blocks = block_tables.shape
+    _on_current_device(block_tables)
+    i32 = torch.int32
+    _int_tensor(block_tables, i32, (B, max_blocks), "block_tables", block_tables)
+    for name, t in (("seq_lens", seq_lens), ("add_len", add_len), ("new_lens", new_lens)):
+        _int_tensor(t, i32, (B,), name, block_tables)
+    for name, t in (("free_top", free_top), ("new_top", new_top), ("dev_status", dev_status)):
+        _int_tensor(t, i32, (1,), name, block_tables)
+    _int_tensor(free_stack, i32, (free_stack.numel(),), "free_stack", block_tables)
+    _int_tensor(row_off, i32, (B + 1,), "row_off", block_tables)
+    capacity = 0
+    if slot_map is not None:
+        capacity = slot_map.numel()
+        _int_tensor(slot_map, torch.int64, (capacity,), "slot_map", block_tables)
+    rc = _lib.spec_extend_paged(
+        B, block_size, max_blocks, _ptr(block_tables), _ptr(seq_lens), _ptr(add_len),
+        _ptr(free_stack), _ptr(free_top), free_stack.numel(), _ptr(new_lens), _ptr(new_top),
+        _ptr(row_off), _ptr(slot_map), capacity, _ptr(dev_status), _stream(stream))
+    _check("spec_extend_paged", rc)
+
+
+def _token_rows(t, shape, dtype, device, name):
+    """Row stride (elements) of a [T, heads, head_dim] tensor whose rows are
+    contiguous."""
+    T, H, D = shape
+    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be {dtype} {list(shape)} on {device}")
+    if T * H * D and (t.stride(2) != 1 and D > 1 or t.stride(1) != D and H > 1):
+        raise ValueError(f"each row of {name} must be contiguous")
+    return t.stride(0) if T > 1 else H * D
+
+
+def _pool_sizes(kv_pool, layer, like):
+    """[num_blocks, layers, 2, block_size, kv_heads, head_dim] of a pool."""
+    if kv_pool.dim() != 6 or kv_pool.shape[2] != 2 or not kv_pool.is_contiguous() or \
+            kv_pool.dtype != like.dtype or kv_pool.device != like.device:
+        raise ValueError("kv_pool must be contiguous [num_blocks, layers, 2, block_size, "
+                         f"kv_heads, head_dim], {like.dtype} on {like.device}")
+    N, layers, _, bs, H, D = kv_pool.shape
+    if not 0 <= layer < layers:
+        raise ValueError(f"layer {layer} outside the pool's {layers}")
+    return N, layers, bs, H, D
+
+
+def spec_store_kv(k, v, slot_map, kv_pool, layer, dev_status, stream=None):
+    """Store the rows k, v [T, kv_heads, head_dim] (2-byte elements, contiguous
+    rows at any stride) at their slots of one layer of kv_pool [num_blocks,
+    layers, 2, block_size, kv_heads, head_dim]; slots of -1 are skipped."""
+    _on_current_device(k)
+    if k.element_size() != 2:
+        raise TypeError(f"K/V rows must have 2-byte elements, got {k.dtype}")
+    N, layers, bs, H, D = _pool_sizes(kv_pool, layer, k)
+    shape = (k.shape[0], H, D)
+    ld_k = _token_rows(k, shape, k.dtype, k.device, "k")
+    ld_v = _token_rows(v, shape, k.dtype, k.device, "v")
+    _int_tensor(slot_map, torch.int64, (shape[0],), "slot_map", k)
+    rc = _lib.spec_store_kv(_ptr(k), ld_k, _ptr(v), ld_v, shape[0], _ptr(slot_map),
+                            _ptr(kv_pool), N, layers, layer, bs, H, D, _ptr(dev_status),
+                            _stream(stream))
+    _check("spec_store_kv", rc)
+
+
+def spec_attend_workspace_bytes(head_dim):
+    return int(_lib.spec_attend_workspace_bytes(head_dim))
+
+
+def attend_workspace(head_dim, device="cuda"):
+    """A workspace tensor of the size an attention call needs."""
+    n = spec_attend_workspace_bytes(head_dim)
+    if n == 0:
+        raise ValueError("invalid sizes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _attend_dtype(q):
+    if q.dtype == torch.bfloat16:
+        return SPEC_BF16
+    if q.dtype == torch.float16:
+        return SPEC_F16
+    raise TypeError(f"attention takes bfloat16 or float16, got {q.dtype}")
+
+
+def _attend_common(q, out, lse, row_off, ws):
+    _on_current_device(q)
+    code = _attend_dtype(q)
+    T, Hq, D = shape = tuple(q.shape)
+    ld_q = _token_rows(q, shape, q.dtype, q.device, "q")
+    ld_out = _token_rows(out, shape, q.dtype, q.device, "out")
+    if lse is not None:
+        _int_tensor(lse, torch.float32, (T, Hq), "lse", q)
+    if row_off is not None:
+        _int_tensor(row_off, torch.int32, (row_off.numel(),), "row_off", q)
+        if row_off.numel() < 1:
+            raise ValueError("row_off must be int32 [B+1]")
+    if ws.device != q.device:
+        raise ValueError(f"the workspace must be on {q.device}")
+    return code, T, Hq, D, ld_q, ld_out
+
+
+def spec_attend_prompt(q, k, v, row_off, out, dev_status, ws, scale=None, lse=None, stream=None):
+    """Causal attention of packed prompts: q, out [T, q_heads, head_dim],
+    k, v [T, kv_heads, head_dim] (bfloat16 or float16, contiguous rows at any
+    stride), row_off int32 [B+1]; scale defaults to head_dim ** -0.5; lse optional float32
+    [T, q_heads]."""
+    code, T, Hq, D, ld_q, ld_out = _attend_common(q, out, lse, row_off, ws)
+    shape = (T, k.shape[1], D)
+    ld_k = _token_rows(k, shape, q.dtype, q.device, "k")
+    ld_v = _token_rows(v, shape, q.dtype, q.device, "v")
+    rc = _lib.spec_attend_prompt(
+        _ptr(q), ld_q, _ptr(k), ld_k, _ptr(v), ld_v, code, _ptr(row_off), row_off.numel() - 1, T,
+        Hq, k.shape[1], D, D ** -0.5 if scale is None else scale, _ptr(out), ld_out, _ptr(lse),
+        _ptr(dev_status), _ptr(ws), ws.numel(), _stream(stream))
+    _check("spec_attend_prompt", rc)
+
+
+def spec_attend_paged(q, kv_pool, layer, block_tables, seq_lens, out, dev_status, ws,
+                      row_off=None, kv_stage=None, scale=None, lse=None, stream=None):
+    """Attention of new rows over one layer of the paged cache. q, out
+    [T, q_heads, head_dim]: packed by row_off int32 [B+1], or (row_off None) the
+    same number of rows for each sequence; kv_pool as for spec_commit_paged;
+    kv_stage [B, Kp1, layers, 2, kv_heads, head_dim] if the new rows' K/V are
+    staged, None if seq_lens counts them already."""
+    code, T, Hq, D, ld_q, ld_out = _attend_common(q, out, lse, row_off, ws)
+    N, layers, bs, H, Dp = _pool_sizes(kv_pool, layer, q)
+    if Dp != D:
+        raise ValueError("q and kv_pool have different head sizes")
+    B, max_blocks = block_tables.shape
+    _int_tensor(block_tables, torch.int32, (B, max_blocks), "block_tables", q)
+    _int_tensor(seq_lens, torch.int32, (B,), "seq_lens", q)
+    if row_off is not None and row_off.numel() != B + 1:
+        raise ValueError("row_off must be int32 [B+1]")
+    if row_off is None and B and T % B:
+        raise ValueError("without row_off, q holds the same number of rows for each sequence")
+    Kp1 = 0
+    if kv_stage is not None:
+        Kp1 = kv_stage.shape[1]
+        if tuple(kv_stage.shape) != (B, Kp1, layers, 2, H, D) or kv_stage.dtype != q.dtype or \
+                not kv_stage.is_contiguous() or kv_stage.device != q.device:
+            raise ValueError("kv_stage must be contiguous [B, Kp1, layers, 2, kv_heads, head_dim]")
+    rc = _lib.spec_attend_paged(
+        _ptr(q), ld_q, code, _ptr(row_off), T // B if B else 0, B, T, Hq, _ptr(kv_pool), N,
+        layers, layer, bs, H, D, _ptr(block_tables), max_blocks, _ptr(seq_lens), _ptr(kv_stage),
+        Kp1, D ** -0.5 if scale is None else scale, _ptr(out), ld_out, _ptr(lse),
+        _ptr(dev_status), _ptr(ws), ws.numel(), _stream(stream))
+    _check("spec_attend_paged", rc)
 
 
 def spec_verify_chain_commit(tgt, drf, draft_tok, temperature, seed, seq_id, rnd, accept_len,

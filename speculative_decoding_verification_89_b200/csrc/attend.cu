@@ -1,0 +1,789 @@
+// Attention of packed query rows over packed or paged keys and values:
+//   o_i = sum_{j <= len-n+i} p_ij v_j,  p_ij = softmax_j(scale * q_i . k_j)
+// in one pass over the keys: with a running reference m and sum l,
+//   p~ = 2^(c s - m),  l += sum p~,  O += P~ V,  o = O / l,
+// c = scale * log2(e). The reference need not be the running maximum: it is
+// raised (and l, O scaled down) only when a maximum passes it by more than
+// 2^kSlack, so p~ stays below 2^kSlack and the scaling of O is rare.
+//
+// HiSpec (gist.science summary of arXiv 2510.01336), section 2
+// "Unterstuetzung fuer Batch-Inferenz" (paged attention with block tables) and
+// "Wiederverwendung von KV-Cache und versteckten Zustaenden" (K/V rows staged
+// while drafting, kept or dropped by the check).
+//
+// One persistent CTA per SM takes a run of K/V tiles (attend_plan.cuh). Of its
+// three warpgroups the first two are softmax warps, one thread per row of a
+// 128-row tile; in the third, one thread issues the matrix instructions
+// (tcgen05, accumulators in tensor memory) and three warps load. Scores S =
+// Q K^T of a tile land in tensor memory; its warpgroup turns them into P~ in
+// place (two-byte elements over the same columns), which the next instruction
+// reads as its left operand for O += P~ V. While one warpgroup works on its
+// scores, the tensor cores form the other's.
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "attend.cuh"
+#include "kernels.cuh"
+#include "tc05.cuh"
+
+namespace specv {
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kLoaders = 96;      // warps 9-11
+constexpr int kTmemCols = 512;    // S0 S1 O0 O1
+constexpr float kSlack = 8.0f;    // log2 of the largest p~
+
+template <int DP>
+struct Tile {
+  static constexpr int kBytes = 128 * DP * 2;
+  static constexpr int kStages = DP == 128 ? 5 : 10;
+  static constexpr int kSmemTiles = (2 + kStages) * kBytes;
+};
+
+struct Shared {
+  uint64_t kv_full[10], kv_empty[10];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t o_empty, swap, drain;
+  uint32_t tmem;
+  int abort;
+  long long warp_sum[kThreads / 32];
+  int start[4];       // sequence, head, unit, cost taken of it
+  long long run;      // cost of this CTA's run
+  float2 ml[2][kTileRows];
+};
+static_assert(Tile<128>::kSmemTiles + sizeof(Shared) <= 227 * 1024, "shared memory");
+
+// A wait on a barrier phase, at most kWaitLimitNs; a wait that runs out (or
+// another's that did) ends the CTA's work.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Shared* sh,
+                                         int32_t* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*(volatile int*)&sh->abort) return false;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      *(volatile int*)&sh->abort = 1;
+      set_status(status, SPEC_ETIMEOUT);
+      return false;
+    }
+  }
+}
+
+// Sequence b, with what is invalid made empty.
+struct SeqOf {
+  const AttendArgs* a;
+  __device__ AttendSeq operator()(int b) const { return get(b, nullptr); }
+  __device__ AttendSeq get(int b, int* bad) const {
+    AttendSeq s;
+    if (a->row_off) {
+      const int lo = a->row_off[b], hi = a->row_off[b + 1];
+      s.row0 = lo;
+      s.n = hi - lo;
+      if (lo < 0 || hi < lo || hi > a->T) {
+        s.row0 = s.n = 0;
+        if (bad) *bad = 1;
+      }
+    } else {
+      s.row0 = b * a->rows_per_seq;
+      s.n = a->rows_per_seq;
+    }
+    if (!a->tables) {
+      s.len = s.n;
+      return s;
+    }
+    s.len = a->seq_lens[b];
+    if (s.len < 0 || s.len > a->max_blocks * a->block_size || (a->stage_k && s.n > a->stage_rows)) {
+      s.len = 0;
+      if (bad) *bad = 1;
+    } else if (a->stage_k) {
+      s.len += s.n;
+    }
+    return s;
+  }
+};
+
+using Cursor = AttendCursor<SeqOf>;
+
+// Where this CTA's run of the cost line starts, into sh; all threads.
+__device__ void find_run(const AttendArgs& a, AttendShape shape, Shared* sh) {
+  const SeqOf seq{&a};
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.B + kThreads - 1) / kThreads;
+  const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+  long long sum = 0;
+  int bad = 0;
+  for (int b = b0; b < b1; ++b) {
+    const AttendSeq s = seq.get(b, &bad);
+    sum += shape.head_cost(s) * a.kv_heads;
+  }
+  if (bad && blockIdx.x == 0) set_status(a.status, SPEC_EDEVICE);
+  long long incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) sh->warp_sum[warp] = incl;
+  __syncthreads();
+  long long before = 0, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += sh->warp_sum[w];
+    total += sh->warp_sum[w];
+  }
+  const long long share = (total + gridDim.x - 1) / gridDim.x;
+  const long long from = share * blockIdx.x;
+  const long long to = min(total, from + share);
+  if (tid == 0 && from >= to) sh->run = 0;
+  long long at = before + incl - sum;
+  if (from < to && from >= at && from < at + sum) {
+    for (int b = b0; b < b1; ++b) {
+      const AttendSeq s = seq(b);
+      const long long head = shape.head_cost(s);
+      if (from < at + head * a.kv_heads) {
+        const int h = (int)((from - at) / head);
+        const long long y = from - at - h * head;
+        int lo = 0, hi = shape.units(s) - 1;  // the unit u with cost_before(u) <= y
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (shape.cost_before(s, mid) <= y) lo = mid; else hi = mid - 1;
+        }
+        sh->start[0] = b;
+        sh->start[1] = h;
+        sh->start[2] = lo;
+        sh->start[3] = (int)(y - shape.cost_before(s, lo));
+        sh->run = to - from;
+        break;
+      }
+      at += head * a.kv_heads;
+    }
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ Cursor cursor(const AttendArgs& a, AttendShape shape, const Shared* sh) {
+  return Cursor(shape, SeqOf{&a}, a.B, a.kv_heads, sh->start[0], sh->start[1], sh->start[2],
+                sh->start[3], sh->run);
+}
+
+// A ring position: slot and the parity of its phase.
+template <int N>
+struct Ring {
+  int i = 0;
+  uint32_t ph = 0;
+  __device__ void step() {
+    if (++i == N) {
+      i = 0;
+      ph ^= 1;
+    }
+  }
+};
+
+// Tiles of a unit that its first 128-row tile needs (two-tile units).
+__device__ __forceinline__ int first_tile_count(const AttendShape& shape, const AttendPiece& p) {
+  const int nt0 = shape.tiles_upto(p.s, p.tok0 + shape.tpt - 1);
+  return max(0, min(p.t1, nt0) - p.t0);
+}
+
+// ---------------------------------------------------------------------------
+// Loading: query rows, then K and V tiles in the order they are used
+// ---------------------------------------------------------------------------
+template <int DP>
+struct Loader {
+  static constexpr int kChunks = DP / 8;                // 16-byte chunks of a row
+  static constexpr int kRowStep = kLoaders / kChunks;   // rows between a thread's rows
+  const AttendArgs& a;
+  Shared* sh;
+  uint32_t tiles;   // shared address of the tiles
+  int lt;           // 0 .. 95
+  Ring<Tile<DP>::kStages> kv;
+  Ring<2> q;
+
+  __device__ uint32_t chunk_addr(uint32_t tile, int row) const {
+    const int c = lt % kChunks;
+    return tile + (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+  }
+  __device__ bool load_q(const AttendPiece& p, int tok0, int ntok, int tpt) {
+    if (!wait_bar(&sh->q_empty[q.i], q.ph ^ 1, sh, a.status)) return false;
+    const uint32_t tile = tiles + q.i * Tile<DP>::kBytes;
+    const int c = lt % kChunks;
+    const int rows = min(ntok, tpt) * a.group;
+    for (int r = lt / kChunks; r < 128; r += kRowStep) {
+      const int t = r / a.group, g = r - t * a.group;
+      const bool ok = r < rows && c * 8 < a.dim;
+      const unsigned char* src =
+          a.q + (ok ? (p.s.row0 + tok0 + t) * a.ld_q +
+                          ((long long)(p.h * a.group + g) * a.dim + c * 8) * 2
+                    : 0);
+      cp_async16(chunk_addr(tile, r), src, ok ? 16u : 0u);
+    }
+    cp_async_arrive(&sh->q_full[q.i]);
+    q.step();
+    return true;
+  }
+  // K (v = 0) or V (v = 1) rows [key0, key0 + 128) of piece p's sequence;
+  // rows past its keys are zeros, so what lies there cannot reach a product.
+  __device__ bool load_kv(const AttendPiece& p, int t, int v) {
+    if (!wait_bar(&sh->kv_empty[kv.i], kv.ph ^ 1, sh, a.status)) return false;
+    const uint32_t tile = tiles + (2 + kv.i) * Tile<DP>::kBytes;
+    const int c = lt % kChunks;
+    const long long col = ((long long)p.h * a.dim + c * 8) * 2;
+    const unsigned char* base = v ? a.v : a.k;
+    const long long ld = v ? a.ld_v : a.ld_k;
+    const int pooled = a.stage_k ? p.s.len - p.s.n : p.s.len;
+    const int32_t* table = a.tables ? a.tables + (long long)p.b * a.max_blocks : nullptr;
+#pragma unroll 4
+    for (int r = lt / kChunks; r < 128; r += kRowStep) {
+      const int key = t * kTileKeys + r;
+      bool ok = key < p.s.len && c * 8 < a.dim;
+      const unsigned char* src = base;
+      if (ok) {
+        if (!table) {
+          src = base + (p.s.row0 + key) * ld + col;
+        } else if (key < pooled) {
+          const int blk = key / a.block_size;
+          const int id = table[blk];
+          if (id < 0 || id >= a.num_blocks) {
+            ok = false;
+            set_status(a.status, SPEC_EDEVICE);
+          } else {
+            src = base + id * a.page_bytes + (key - blk * a.block_size) * ld + col;
+          }
+        } else {
+          src = (v ? a.stage_v : a.stage_k) + p.b * a.stage_seq + (key - pooled) * a.stage_row + col;
+        }
+      }
+      cp_async16(chunk_addr(tile, r), src, ok ? 16u : 0u);
+    }
+    cp_async_arrive(&sh->kv_full[kv.i]);
+    kv.step();
+    return true;
+  }
+  __device__ void run(AttendShape shape) {
+    Cursor cur = cursor(a, shape, sh);
+    AttendPiece p;
+    while (cur.next(&p)) {
+      const int m = p.t1 - p.t0;
+      if (m == 0) continue;
+      const bool two = p.ntok > shape.tpt;
+      if (!load_q(p, p.tok0, p.ntok, shape.tpt)) return;
+      if (two && !load_q(p, p.tok0 + shape.tpt, p.ntok - shape.tpt, shape.tpt)) return;
+      const int ahead = two ? 1 : 2;  // K tiles used before the first V tile
+      for (int i = 0; i < min(ahead, m); ++i)
+        if (!load_kv(p, p.t0 + i, 0)) return;
+      for (int i = 0; i < m; ++i) {
+        if (!load_kv(p, p.t0 + i, 1)) return;
+        if (i + ahead < m && !load_kv(p, p.t0 + i + ahead, 0)) return;
+      }
+    }
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Matrix instructions, issued by one thread
+// ---------------------------------------------------------------------------
+template <typename T, int DP>
+struct Issuer {
+  static constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
+  static constexpr uint32_t kIdescQK = mma_idesc(kBf, 128, 128, false);
+  static constexpr uint32_t kIdescPV = mma_idesc(kBf, 128, DP, true);
+  const AttendArgs& a;
+  Shared* sh;
+  uint32_t tiles, tmem;
+  Ring<Tile<DP>::kStages> kv;
+  Ring<2> q;
+  uint32_t p_ph[2];
+  uint32_t pieces;
+
+  __device__ bool wait(uint64_t* bar, uint32_t ph) { return wait_bar(bar, ph, sh, a.status); }
+  // The next K or V tile in shared memory (its address in *addr).
+  __device__ bool acquire(uint32_t* addr) {
+    if (!wait(&sh->kv_full[kv.i], kv.ph)) return false;
+    fence_proxy_async_smem();
+    *addr = tiles + (2 + kv.i) * Tile<DP>::kBytes;
+    return true;
+  }
+  __device__ void release() {
+    tc_commit(&sh->kv_empty[kv.i]);
+    kv.step();
+  }
+  __device__ uint32_t s_col(int w) const { return tmem + w * 128; }
+  __device__ uint32_t o_col(int w) const { return tmem + 256 + w * DP; }
+  // S_w = Q K^T
+  __device__ void qk(int w, uint32_t qaddr, uint32_t kaddr) {
+#pragma unroll
+    for (int k = 0; k < DP / 16; ++k) {
+      const uint32_t off = (k >> 2) * (128 * 128) + (k & 3) * 32;
+      mma_ss(s_col(w), mma_sdesc(qaddr + off, 16), mma_sdesc(kaddr + off, 16), kIdescQK, k > 0);
+    }
+    tc_commit(&sh->s_full[w]);
+  }
+  // O_w (+)= P_w V
+  __device__ bool pv(int w, uint32_t vaddr, bool acc) {
+    if (!wait(&sh->p_full[w], p_ph[w])) return false;
+    p_ph[w] ^= 1;
+    tc_fence_after();
+#pragma unroll
+    for (int k = 0; k < kTileKeys / 16; ++k)
+      mma_ts(o_col(w), s_col(w) + k * 8, mma_sdesc(vaddr + k * (16 * 128), 128 * 128), kIdescPV,
+             acc || k > 0);
+    return true;
+  }
+  __device__ bool piece(const AttendShape& shape, const AttendPiece& p) {
+    const int m = p.t1 - p.t0;
+    const bool two = p.ntok > shape.tpt;
+    uint32_t qa[2], ka, va;
+    int qs[2];
+    if (m > 0) {
+      for (int w = 0; w < (two ? 2 : 1); ++w) {
+        if (!wait(&sh->q_full[q.i], q.ph)) return false;
+        fence_proxy_async_smem();
+        qa[w] = tiles + q.i * Tile<DP>::kBytes;
+        qs[w] = q.i;
+        q.step();
+      }
+    }
+    if (m > 0 && two) {
+      const int c0 = first_tile_count(shape, p);
+      if (!acquire(&ka)) return false;
+      if (c0 > 0) qk(0, qa[0], ka);
+      if (c0 <= 1) tc_commit(&sh->q_empty[qs[0]]);
+      qk(1, qa[1], ka);
+      release();
+      if (m == 1) tc_commit(&sh->q_empty[qs[1]]);
+    } else if (m > 0) {
+      for (int i = 0; i < min(2, m); ++i) {
+        if (!acquire(&ka)) return false;
+        qk(i, qa[0], ka);
+        release();
+      }
+      if (m <= 2) tc_commit(&sh->q_empty[qs[0]]);
+    }
+    // The accumulators are free once the softmax warps have read the last piece's.
+    if (pieces > 0 && !wait(&sh->o_empty, (pieces - 1) & 1)) return false;
+    ++pieces;
+    tc_fence_after();
+    if (m == 0) return true;
+    if (two) {
+      const int c0 = first_tile_count(shape, p);
+      for (int i = 0; i < m; ++i) {
+        if (!acquire(&va)) return false;
+        const int vstage = kv.i;
+        kv.step();
+        if (i < c0) {
+          if (!pv(0, va, i > 0)) return false;
+          if (i == c0 - 1) tc_commit(&sh->o_full[0]);
+        }
+        if (i + 1 < m) {
+          if (!acquire(&ka)) return false;
+          if (i + 1 < c0) qk(0, qa[0], ka);
+          if (i + 1 == c0 - 1) tc_commit(&sh->q_empty[qs[0]]);
+        }
+        if (!pv(1, va, i > 0)) return false;
+        tc_commit(&sh->kv_empty[vstage]);
+        if (i == m - 1) tc_commit(&sh->o_full[1]);
+        if (i + 1 < m) {
+          qk(1, qa[1], ka);
+          release();
+          if (i + 1 == m - 1) tc_commit(&sh->q_empty[qs[1]]);
+        }
+      }
+    } else {
+      for (int i = 0; i < m; ++i) {
+        const int w = i & 1;
+        if (!acquire(&va)) return false;
+        if (!pv(w, va, i > 1)) return false;
+        if (i + 2 >= m) tc_commit(&sh->o_full[w]);
+        release();
+        if (i + 2 < m) {
+          if (!acquire(&ka)) return false;
+          qk(w, qa[0], ka);
+          release();
+          if (i + 2 == m - 1) tc_commit(&sh->q_empty[qs[0]]);
+        }
+      }
+    }
+    return true;
+  }
+  __device__ void run(AttendShape shape) {
+    Cursor cur = cursor(a, shape, sh);
+    AttendPiece p;
+    while (cur.next(&p))
+      if (!piece(shape, p)) {
+        // Instructions in flight end before tensor memory is given back.
+        tc_commit(&sh->drain);
+        mbar_wait_bounded(&sh->drain, 0, kWaitLimitNs);
+        return;
+      }
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Softmax and output, one thread per row
+// ---------------------------------------------------------------------------
+template <typename T> struct Pack;
+template <> struct Pack<__nv_bfloat16> {
+  static __device__ __forceinline__ uint32_t two(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
+};
+template <> struct Pack<__half> {
+  static __device__ __forceinline__ uint32_t two(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
+};
+
+__device__ __forceinline__ float weight(float m, float ref) {
+  return m == -INFINITY ? 0.0f : ex2(m - ref);
+}
+
+template <typename T, int DP>
+struct Softmax {
+  const AttendArgs& a;
+  Shared* sh;
+  uint32_t tmem;    // with this warp's lanes
+  int w, row;       // warpgroup, row of the tile
+  int tok, head;    // row's token within a tile and query head within the group
+  uint32_t s_ph, o_ph[2], x_ph;
+
+  __device__ bool wait(uint64_t* bar, uint32_t ph) {
+    return __all_sync(0xffffffffu, wait_bar(bar, ph, sh, a.status));
+  }
+  __device__ void arrive(uint64_t* bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+  }
+  // Scores of one tile to p~; m is the reference and l the sum, both of this row.
+  __device__ bool tile(int key0, int limit, int warp_limit, bool live, bool first, float& m,
+                       float& l) {
+    if (!wait(&sh->s_full[w], s_ph)) return false;
+    s_ph ^= 1;
+    if (live) {
+      tc_fence_after();
+      uint32_t s[128];
+      const uint32_t col = tmem + w * 128;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tmem_ld32(col + 32 * i, s, 32 * i);
+      tmem_wait_ld(s);
+      if (key0 + kTileKeys - 1 > warp_limit) {
+        const int lim = limit - key0;
+#pragma unroll
+        for (int i = 0; i < 128; ++i)
+          if (i > lim) s[i] = 0xff800000u;
+      }
+      float mx[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(s[i]);
+#pragma unroll
+      for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
+      const float top =
+          fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+      const bool raise = top > m + kSlack || (m == -INFINITY && top > m);
+      if (__any_sync(0xffffffffu, raise)) {
+        const float f = weight(m, fmaxf(m, top));
+        m = fmaxf(m, top);
+        l *= f;
+        if (!first) {  // the products up to the last tile's are in O
+#pragma unroll 1
+          for (int c = 0; c < DP; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(tmem + 256 + w * DP + c, o, 0);
+            tmem_wait_ld(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st32(tmem + 256 + w * DP + c, o, 0);
+          }
+        }
+      }
+      const float ref = m == -INFINITY ? 0.0f : m;
+      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < 128; i += 64) {
+        uint32_t p[32];
+#pragma unroll
+        for (int j = 0; j < 64; j += 2) {
+          const float e0 = ex2(fmaf(__uint_as_float(s[i + j]), a.scale_log2, -ref));
+          const float e1 = ex2(fmaf(__uint_as_float(s[i + j + 1]), a.scale_log2, -ref));
+          sum[j & 2] += e0;
+          sum[(j & 2) + 1] += e1;
+          p[j / 2] = Pack<T>::two(e0, e1);
+        }
+        tmem_st32(col + i / 2, p, 0);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_wait_st();
+      tc_fence_before();
+    }
+    arrive(&sh->p_full[w]);
+    return true;
+  }
+  // Columns [c0, c0 + 32) of f0 * O0 + f1 * O1; all lanes. A factor of 0 drops its
+  // part whatever it holds (rows that saw no key there, beside values not finite).
+  __device__ void read_o(int c0, bool has0, float f0, bool has1, float f1, float (&o)[32]) {
+    uint32_t x[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+    if (has0) {
+      tmem_ld32(tmem + 256 + c0, x, 0);
+      tmem_wait_ld(x);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = f0 == 0.0f ? 0.0f : f0 * __uint_as_float(x[i]);
+    }
+    if (has1) {
+      tmem_ld32(tmem + 256 + DP + c0, x, 0);
+      tmem_wait_ld(x);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = f1 == 0.0f ? o[i] : fmaf(f1, __uint_as_float(x[i]), o[i]);
+    }
+  }
+  __device__ void write_out(unsigned char* dst, int c0, const float (&o)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+      if (c0 + i < a.dim)
+        *reinterpret_cast<uint4*>(dst + (c0 + i) * 2) =
+            make_uint4(Pack<T>::two(o[i], o[i + 1]), Pack<T>::two(o[i + 2], o[i + 3]),
+                       Pack<T>::two(o[i + 4], o[i + 5]), Pack<T>::two(o[i + 6], o[i + 7]));
+  }
+  __device__ void run(AttendShape shape) {
+    Cursor cur = cursor(a, shape, sh);
+    AttendPiece p;
+    AttendRec rec = {};
+    bool skipped = false;  // a phase of the other accumulator's barrier not yet waited for
+    while (cur.next(&p)) {
+      if (skipped) {
+        if (!wait(&sh->o_full[w ^ 1], o_ph[w ^ 1])) return;
+        o_ph[w ^ 1] ^= 1;
+        skipped = false;
+      }
+      const int m_tiles = p.t1 - p.t0;
+      const bool two = p.ntok > shape.tpt;
+      const int base = two ? w * shape.tpt : 0;  // the tile's first token in the unit
+      const int ntok = min(shape.tpt, p.ntok - base);
+      const bool valid = tok < ntok;
+      const bool live = __any_sync(0xffffffffu, valid);
+      const int limit = valid ? p.s.len - p.s.n + p.tok0 + base + tok : INT32_MAX;
+      const int warp_limit = __reduce_min_sync(0xffffffffu, limit);
+      const int c0 = two ? first_tile_count(shape, p) : (m_tiles + 1) / 2;
+      const int c1 = two ? m_tiles : m_tiles / 2;
+      const int mine = w ? c1 : c0;
+      float m = -INFINITY, l = 0.0f;
+      for (int i = 0; i < mine; ++i) {
+        const int t = p.t0 + (two ? i : 2 * i + w);
+        if (!tile(t * kTileKeys, limit, warp_limit, live, i == 0, m, l)) return;
+      }
+      if (p.t0 > 0) {
+        rec.first = 1;
+        rec.first_cont = p.t1 < p.nt;
+      } else if (p.t1 < p.nt) {
+        rec.head = 1;
+        rec.row0 = p.s.row0;
+        rec.tok0 = p.tok0;
+        rec.ntok = p.ntok;
+        rec.h = p.h;
+      }
+      const bool whole = p.t0 == 0 && p.t1 == p.nt;
+      const long long slot = 2 * blockIdx.x + (p.t0 > 0 ? 0 : 1);
+      const long long prow = (slot * 2 + (two ? w : 0)) * kTileRows + row;
+      const int r = p.s.row0 + p.tok0 + base + tok;
+      const int qh = p.h * a.group + head;
+      unsigned char* dst = a.out + r * a.ld_out + (long long)qh * a.dim * 2;
+      float f0 = w == 0 ? 1.0f : 0.0f, f1 = 1.0f - f0;
+      int from = 0, to = DP;
+      bool has0 = w == 0 && c0 > 0, has1 = w == 1 && c1 > 0;
+      for (int x = 0; x < 2; ++x)
+        if ((two ? x == w : true) && (x ? c1 : c0) > 0) {
+          if (!wait(&sh->o_full[x], o_ph[x])) return;
+          o_ph[x] ^= 1;
+        }
+      skipped = two && (w ? c0 : c1) > 0;
+      if (!two) {  // both warpgroups hold part of every row: join, half the columns each
+        sh->ml[w][row] = make_float2(m, l);
+        arrive(&sh->swap);
+        if (!wait(&sh->swap, x_ph)) return;
+        x_ph ^= 1;
+        const float2 u = sh->ml[w ^ 1][row];
+        arrive(&sh->swap);
+        if (!wait(&sh->swap, x_ph)) return;
+        x_ph ^= 1;
+        const float top = fmaxf(m, u.x);
+        const float fm = weight(m, top), fu = weight(u.x, top);
+        f0 = w ? fu : fm;
+        f1 = w ? fm : fu;
+        l = fm * l + fu * u.y;
+        m = top;
+        has0 = c0 > 0;
+        has1 = c1 > 0;
+        from = w * (DP / 2);
+        to = from + DP / 2;
+      }
+      if (live) {
+        tc_fence_after();
+        if (whole) {
+          const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+          f0 *= inv;
+          f1 *= inv;
+        }
+#pragma unroll 1
+        for (int c = from; c < to; c += 32) {
+          float o[32];
+          read_o(c, has0, f0, has1, f1, o);
+          if (valid && whole) write_out(dst, c, o);
+          if (valid && !whole) {
+            float4* po = reinterpret_cast<float4*>(a.part_o + prow * DP + c);
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              po[i / 4] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          }
+        }
+        if (valid && (two || w == 0)) {
+          if (!whole) a.part_ml[prow] = make_float2(m, l);
+          else if (a.lse)
+            a.lse[(long long)r * a.q_heads + qh] =
+                l > 0.0f || l != l ? (float)((m + log2f(l)) * kLn2) : -INFINITY;
+        }
+        tc_fence_before();
+      }
+      arrive(&sh->o_empty);
+    }
+    if (threadIdx.x == 0) a.rec[blockIdx.x] = rec;
+  }
+};
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_constant__ AttendArgs a) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  Shared* sh = reinterpret_cast<Shared*>(smem + Tile<DP>::kSmemTiles);
+  const int tid = threadIdx.x, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < Tile<DP>::kStages; ++i) {
+      mbar_init(&sh->kv_full[i], kLoaders);
+      mbar_init(&sh->kv_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->q_full[i], kLoaders);
+      mbar_init(&sh->q_empty[i], 1);
+      mbar_init(&sh->s_full[i], 1);
+      mbar_init(&sh->p_full[i], 4);
+      mbar_init(&sh->o_full[i], 1);
+    }
+    mbar_init(&sh->o_empty, 8);
+    mbar_init(&sh->swap, 8);
+    mbar_init(&sh->drain, 1);
+    sh->abort = 0;
+    sh->run = 0;
+    fence_barrier_init();
+  }
+  pdl_begin();
+  if (warp == 8) tmem_alloc(&sh->tmem, kTmemCols);
+  const AttendShape shape{kTileRows / a.group};
+  tc_fence_before();
+  find_run(a, shape, sh);  // its barriers publish the above
+  tc_fence_after();
+  const uint32_t tiles = smem_u32(smem), tmem = sh->tmem;
+  if (warp < 8) {
+    const int row = tid & 127;
+    Softmax<T, DP> s{a, sh, tmem + ((uint32_t)(warp & 3) << 21), warp >> 2, row, row / a.group,
+                     row % a.group, 0, {0, 0}, 0};
+    s.run(shape);
+  } else if (warp == 8) {
+    if ((tid & 31) == 0) {
+      Issuer<T, DP> s{a, sh, tiles, tmem, {}, {}, {0, 0}, 0};
+      s.run(shape);
+    }
+  } else {
+    Loader<DP> s{a, sh, tiles, tid - 9 * 32, {}, {}};
+    s.run(shape);
+    cp_async_wait_all();
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  // After a wait that ran out nothing is combined from this CTA.
+  if (tid == 0 && sh->abort) a.rec[blockIdx.x] = AttendRec{};
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Joining the parts of divided units
+// ---------------------------------------------------------------------------
+constexpr int kCombineThreads = 128;
+constexpr int kCombineSplit = 16;  // blocks per unit
+template <typename T, int DP>
+__global__ void __launch_bounds__(kCombineThreads) attend_combine_kernel(const __grid_constant__ AttendArgs a) {
+  pdl_begin();
+  const int c = blockIdx.x;
+  const AttendRec rec = a.rec[c];
+  if (!rec.head) return;
+  int last = min(c + 1, a.ctas - 1);  // CTAs c .. last hold the unit's parts
+  while (last + 1 < a.ctas && a.rec[last].first && a.rec[last].first_cont) ++last;
+  const int tpt = kTileRows / a.group;
+  const bool two = rec.ntok > tpt;
+  const int lane = threadIdx.x & 31;
+  constexpr int kCols = DP / 32;
+  for (int row = blockIdx.y * (kCombineThreads / 32) + (threadIdx.x >> 5);
+       row < (two ? 2 : 1) * kTileRows; row += kCombineSplit * (kCombineThreads / 32)) {
+    const int w = row / kTileRows, rt = (row % kTileRows) / a.group, g = row % kTileRows % a.group;
+    const int tok = w * tpt + rt;
+    if (rt >= tpt || tok >= rec.ntok) continue;
+    float m = -INFINITY;
+    for (int x = c; x <= last; ++x) {
+      const long long prow = (2LL * x + (x == c ? 1 : 0)) * 2 * kTileRows + row;
+      m = fmaxf(m, a.part_ml[prow].x);
+    }
+    float l = 0.0f, o[kCols];
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) o[i] = 0.0f;
+    for (int x = c; x <= last; ++x) {
+      const long long prow = (2LL * x + (x == c ? 1 : 0)) * 2 * kTileRows + row;
+      const float2 ml = a.part_ml[prow];
+      const float f = weight(ml.x, m);
+      l = fmaf(f, ml.y, l);
+      const float* src = a.part_o + prow * DP + lane * kCols;
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) o[i] = f == 0.0f ? o[i] : fmaf(f, src[i], o[i]);
+    }
+    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+    const int r = rec.row0 + rec.tok0 + tok, qh = rec.h * a.group + g;
+    if (lane * kCols < a.dim) {
+      uint32_t* dst = reinterpret_cast<uint32_t*>(
+          a.out + r * a.ld_out + ((long long)qh * a.dim + lane * kCols) * 2);
+#pragma unroll
+      for (int i = 0; i < kCols; i += 2) dst[i / 2] = Pack<T>::two(o[i] * inv, o[i + 1] * inv);
+    }
+    if (lane == 0 && a.lse)
+      a.lse[(long long)r * a.q_heads + qh] =
+          l > 0.0f || l != l ? (float)((m + log2f(l)) * kLn2) : -INFINITY;
+  }
+}
+
+template <typename T, int DP>
+cudaError_t launch(const AttendArgs& a, cudaStream_t st) {
+  const size_t smem = Tile<DP>::kSmemTiles + sizeof(Shared);
+  cudaError_t e = reserve_dyn_smem(attend_kernel<T, DP>, smem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(attend_kernel<T, DP>, dim3(a.ctas), dim3(kThreads), smem, st, a);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attend_combine_kernel<T, DP>, dim3(a.ctas, kCombineSplit),
+                    dim3(kCombineThreads), 0, st, a);
+}
+
+}  // namespace
+
+cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
+  if (a.dtype == SPEC_BF16)
+    return a.dim <= 64 ? launch<__nv_bfloat16, 64>(a, st) : launch<__nv_bfloat16, 128>(a, st);
+  return a.dim <= 64 ? launch<__half, 64>(a, st) : launch<__half, 128>(a, st);
+}
+
+}  // namespace specv

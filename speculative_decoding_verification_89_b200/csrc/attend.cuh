@@ -1,0 +1,67 @@
+// Arguments and launchers of the attention operators.
+#pragma once
+#include "attend_plan.cuh"
+#include "common.cuh"
+
+namespace specv {
+
+constexpr int kAttendMaxCtas = 148;
+constexpr int kAttendMaxGroup = kTileRows;  // query heads that share a K/V head
+constexpr int kAttendMaxDim = 128;
+
+// What a CTA leaves for the combine launch: whether its run begins inside a
+// unit (slot 2c holds that part) and, if so, whether the unit goes on past the
+// run; whether its last unit begins here and goes on (slot 2c + 1), and which
+// rows that unit has.
+struct AttendRec {
+  int first, first_cont, head;
+  int row0, tok0, ntok, h, pad;
+};
+
+struct AttendArgs {
+  int B, T, q_heads, kv_heads, group, dim;
+  int dtype;          // SPEC_BF16 or SPEC_F16
+  int rows_per_seq;   // rows of each sequence where row_off is NULL
+  const int32_t* row_off;
+  float scale_log2;   // scale * log2(e)
+  const unsigned char* q;
+  long long ld_q;     // bytes between token rows
+  unsigned char* out;
+  long long ld_out;
+  float* lse;
+  // keys and values: packed rows (tables NULL), or the pool at (block 0, layer)
+  const unsigned char* k;
+  const unsigned char* v;
+  long long ld_k, ld_v;   // bytes between token rows (packed), or between a block's rows
+  long long page_bytes;   // bytes between blocks
+  const int32_t* tables;
+  const int32_t* seq_lens;
+  int max_blocks, num_blocks, block_size;
+  // the new rows' own keys and values, staged (NULL: they are in the pool)
+  const unsigned char* stage_k;
+  const unsigned char* stage_v;
+  long long stage_seq, stage_row;  // bytes between sequences, rows
+  int stage_rows;
+  int32_t* status;
+  float* part_o;     // [2 * ctas][2 * kTileRows][DP] unnormalised
+  float2* part_ml;   // [2 * ctas][2 * kTileRows] (maximum in log2 units, sum)
+  AttendRec* rec;    // [ctas]
+  int ctas;
+};
+// Workspace bytes of the parts, for rows padded to DP columns.
+struct AttendWs {
+  size_t o, ml, rec, total;
+};
+inline int attend_padded_dim(int dim) { return dim <= 64 ? 64 : 128; }
+inline AttendWs attend_ws(int dim) {
+  const size_t rows = (size_t)2 * kAttendMaxCtas * 2 * kTileRows;
+  AttendWs w;
+  w.o = 0;
+  w.ml = rows * attend_padded_dim(dim) * sizeof(float);
+  w.rec = w.ml + rows * sizeof(float2);
+  w.total = (w.rec + kAttendMaxCtas * sizeof(AttendRec) + 255) & ~(size_t)255;
+  return w;
+}
+cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st);
+
+}  // namespace specv

@@ -6,8 +6,10 @@
 #include <cstdint>
 #include <cstring>
 
+#include "attend.cuh"
 #include "common.cuh"
 #include "kernels.cuh"
+#include "paged.cuh"
 
 using namespace specv;
 
@@ -123,6 +125,56 @@ int cuda_status(cudaError_t e) {
   if (e == cudaSuccess) return SPEC_OK;
   g_last_cuda = e;
   return SPEC_ECUDA;
+}
+
+// Block pool sizes whose token positions and slots fit the kernels' indices.
+bool pool_sizes_ok(int B, int block_size, int max_blocks, int num_blocks) {
+  return B >= 0 && B <= SPEC_MAX_COMMIT_B && block_size >= 1 && max_blocks >= 1 &&
+         num_blocks >= 1 && (int64_t)max_blocks * block_size <= SPEC_MAX_CONTEXT;
+}
+
+// Rows of 2-byte elements for 16-byte accesses.
+bool half_rows_ok(const void* p, int64_t ld, int64_t row) {
+  return p && aligned(p, 16) && ld >= row && (ld * 2) % 16 == 0;
+}
+
+// The checks and arguments that both attention calls share.
+int attend_args(const void* q, int64_t ld_q, int dtype, const int32_t* row_off, int B, int T,
+                int q_heads, int kv_heads, int head_dim, float scale, void* out, int64_t ld_out,
+                float* lse, int32_t* dev_status, void* ws, size_t ws_bytes, AttendArgs* a) {
+  if (dtype != SPEC_BF16 && dtype != SPEC_F16) return SPEC_EINVAL;
+  if (B < 0 || B > SPEC_MAX_COMMIT_B || T < 0 || T > SPEC_MAX_CONTEXT) return SPEC_EINVAL;
+  if (head_dim < 8 || head_dim > SPEC_MAX_HEAD_DIM || head_dim % 8 || kv_heads < 1 ||
+      q_heads < kv_heads || q_heads % kv_heads || q_heads / kv_heads > kAttendMaxGroup ||
+      q_heads > (1 << 16))
+    return SPEC_EINVAL;
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return SPEC_EINVAL;
+  if (B == 0 || T == 0) return SPEC_OK;
+  const int64_t row = (int64_t)q_heads * head_dim;
+  if (!half_rows_ok(q, ld_q, row) || !half_rows_ok(out, ld_out, row)) return SPEC_EINVAL;
+  const AttendWs w = attend_ws(head_dim);
+  if (!ws || !aligned(ws, kAlign) || ws_bytes < w.total) return SPEC_EWORKSPACE;
+  std::memset(a, 0, sizeof(*a));
+  a->B = B;
+  a->T = T;
+  a->q_heads = q_heads;
+  a->kv_heads = kv_heads;
+  a->group = q_heads / kv_heads;
+  a->dim = head_dim;
+  a->dtype = dtype;
+  a->row_off = row_off;
+  a->scale_log2 = (float)(scale * kLog2e);
+  a->q = (const unsigned char*)q;
+  a->ld_q = ld_q * 2;
+  a->out = (unsigned char*)out;
+  a->ld_out = ld_out * 2;
+  a->lse = lse;
+  a->status = dev_status;
+  a->part_o = reinterpret_cast<float*>((char*)ws + w.o);
+  a->part_ml = reinterpret_cast<float2*>((char*)ws + w.ml);
+  a->rec = reinterpret_cast<AttendRec*>((char*)ws + w.rec);
+  a->ctas = std::min(sm_count(), kAttendMaxCtas);
+  return SPEC_OK;
 }
 
 struct ChainCheck {
@@ -843,6 +895,127 @@ int spec_vp_pick(const void* tgt, int64_t ld_tgt, const void* drf, int64_t ld_dr
   a.out_tok = out_tok;
   a.diag = diag;
   return cuda_status(launch_vp_pick(dtype, a, (cudaStream_t)stream));
+}
+
+int spec_extend_paged(int B, int block_size, int max_blocks, int32_t* block_tables,
+                      const int32_t* seq_lens, const int32_t* add_len, const int32_t* free_stack,
+                      const int32_t* free_top, int num_blocks, int32_t* new_lens,
+                      int32_t* new_top, int32_t* row_off, int64_t* slot_map, int64_t capacity,
+                      int32_t* dev_status, void* stream) {
+  if (!pool_sizes_ok(B, block_size, max_blocks, num_blocks) || capacity < 0) return SPEC_EINVAL;
+  if (B == 0) return SPEC_OK;
+  if (!block_tables || !seq_lens || !add_len || !free_stack || !free_top || !new_lens ||
+      !new_top || !row_off || !dev_status || (slot_map && !aligned(slot_map, 8)))
+    return SPEC_EINVAL;
+  ExtendArgs a;
+  a.B = B;
+  a.block_size = block_size;
+  a.max_blocks = max_blocks;
+  a.num_blocks = num_blocks;
+  a.tables = block_tables;
+  a.seq_lens = seq_lens;
+  a.add_len = add_len;
+  a.free_stack = free_stack;
+  a.free_top = free_top;
+  a.new_lens = new_lens;
+  a.new_top = new_top;
+  a.row_off = row_off;
+  a.slot_map = slot_map;
+  a.cap = capacity;
+  a.status = dev_status;
+  return cuda_status(launch_extend(a, (cudaStream_t)stream));
+}
+
+int spec_store_kv(const void* k, int64_t ld_k, const void* v, int64_t ld_v, int T,
+                  const int64_t* slot_map, void* kv_pool, int num_blocks, int layers, int layer,
+                  int block_size, int kv_heads, int head_dim, int32_t* dev_status,
+                  void* stream) {
+  const int64_t row = (int64_t)kv_heads * head_dim;
+  if (T < 0 || !pool_sizes_ok(1, block_size, 1, num_blocks) || layers < 1 || layer < 0 ||
+      layer >= layers || kv_heads < 1 || head_dim < 1 || row > (1 << 24) || (row * 2) % 16)
+    return SPEC_EINVAL;
+  if (T == 0) return SPEC_OK;
+  if (!half_rows_ok(k, ld_k, row) || !half_rows_ok(v, ld_v, row) || !slot_map ||
+      !aligned(slot_map, 8) || !kv_pool || !aligned(kv_pool, 16))
+    return SPEC_EINVAL;
+  StoreArgs a;
+  a.k = (const unsigned char*)k;
+  a.v = (const unsigned char*)v;
+  a.ld_k = ld_k * 2;
+  a.ld_v = ld_v * 2;
+  a.T = T;
+  a.slot_map = slot_map;
+  a.row_bytes = (int)(row * 2);
+  a.pool = (unsigned char*)kv_pool + (int64_t)layer * 2 * block_size * a.row_bytes;
+  a.page_bytes = (int64_t)layers * 2 * block_size * a.row_bytes;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.status = dev_status;
+  return cuda_status(launch_store_kv(a, (cudaStream_t)stream));
+}
+
+size_t spec_attend_workspace_bytes(int head_dim) {
+  return head_dim < 8 || head_dim > SPEC_MAX_HEAD_DIM || head_dim % 8 ? 0
+                                                                     : attend_ws(head_dim).total;
+}
+
+int spec_attend_prompt(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
+                       int64_t ld_v, int dtype, const int32_t* row_off, int B, int T,
+                       int q_heads, int kv_heads, int head_dim, float scale, void* out,
+                       int64_t ld_out, float* lse, int32_t* dev_status, void* ws,
+                       size_t ws_bytes, void* stream) {
+  AttendArgs a;
+  const int rc = attend_args(q, ld_q, dtype, row_off, B, T, q_heads, kv_heads, head_dim, scale,
+                             out, ld_out, lse, dev_status, ws, ws_bytes, &a);
+  if (rc != SPEC_OK) return rc;
+  const int64_t row = (int64_t)kv_heads * head_dim;
+  if (B == 0 || T == 0) return SPEC_OK;
+  if (!row_off || !half_rows_ok(k, ld_k, row) || !half_rows_ok(v, ld_v, row)) return SPEC_EINVAL;
+  a.k = (const unsigned char*)k;
+  a.v = (const unsigned char*)v;
+  a.ld_k = ld_k * 2;
+  a.ld_v = ld_v * 2;
+  return cuda_status(launch_attend(a, (cudaStream_t)stream));
+}
+
+int spec_attend_paged(const void* q, int64_t ld_q, int dtype, const int32_t* row_off,
+                      int rows_per_seq, int B, int T, int q_heads, const void* kv_pool,
+                      int num_blocks, int layers, int layer, int block_size, int kv_heads,
+                      int head_dim, const int32_t* block_tables, int max_blocks,
+                      const int32_t* seq_lens, const void* kv_stage, int Kp1, float scale,
+                      void* out, int64_t ld_out, float* lse, int32_t* dev_status, void* ws,
+                      size_t ws_bytes, void* stream) {
+  AttendArgs a;
+  const int rc = attend_args(q, ld_q, dtype, row_off, B, T, q_heads, kv_heads, head_dim, scale,
+                             out, ld_out, lse, dev_status, ws, ws_bytes, &a);
+  if (rc != SPEC_OK) return rc;
+  if (!pool_sizes_ok(B, block_size, max_blocks, num_blocks) || layers < 1 || layer < 0 ||
+      layer >= layers || (kv_stage && Kp1 < 1) || Kp1 > (1 << 20) || rows_per_seq < 0)
+    return SPEC_EINVAL;
+  if (!row_off && ((int64_t)B * rows_per_seq != T || (kv_stage && rows_per_seq > Kp1)))
+    return SPEC_EINVAL;
+  if (B == 0 || T == 0) return SPEC_OK;
+  if (!kv_pool || !aligned(kv_pool, 16) || !aligned(kv_stage, 16) || !block_tables || !seq_lens)
+    return SPEC_EINVAL;
+  const int64_t row = (int64_t)kv_heads * head_dim * 2, part = block_size * row;
+  a.rows_per_seq = rows_per_seq;
+  a.k = (const unsigned char*)kv_pool + layer * 2 * part;
+  a.v = a.k + part;
+  a.ld_k = a.ld_v = row;
+  a.page_bytes = layers * 2 * part;
+  a.tables = block_tables;
+  a.seq_lens = seq_lens;
+  a.max_blocks = max_blocks;
+  a.num_blocks = num_blocks;
+  a.block_size = block_size;
+  if (kv_stage) {
+    a.stage_k = (const unsigned char*)kv_stage + layer * 2 * row;
+    a.stage_v = a.stage_k + row;
+    a.stage_row = layers * 2 * row;
+    a.stage_seq = Kp1 * a.stage_row;
+    a.stage_rows = Kp1;
+  }
+  return cuda_status(launch_attend(a, (cudaStream_t)stream));
 }
 
 const char* spec_last_cuda_error(void) { return cudaGetErrorString(g_last_cuda); }
