@@ -202,7 +202,16 @@ struct Loader {
   int lt;           // 0 .. 95
   Ring<Tile<DP>::kStages> kv;
   Ring<2> q;
+  uint32_t issued;
 
+  // After a wait that ran out: the copies in flight land before the CTA ends.
+  __device__ void drain() {
+    for (uint32_t j = 0; j < Tile<DP>::kStages && j < issued; ++j) {
+      const uint32_t n = issued - 1 - j;
+      mbar_wait_bounded(&sh->kv_full[n % Tile<DP>::kStages], (n / Tile<DP>::kStages) & 1,
+                        kWaitLimitNs);
+    }
+  }
   __device__ uint32_t chunk_addr(uint32_t tile, int row) const {
     const int c = lt % kChunks;
     return tile + (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
@@ -225,43 +234,78 @@ struct Loader {
     q.step();
     return true;
   }
-  // K (v = 0) or V (v = 1) rows [key0, key0 + 128) of piece p's sequence;
-  // rows past its keys are zeros, so what lies there cannot reach a product.
+  // K (v = 0) or V (v = 1) rows of tile t of piece p's sequence. A tile whose
+  // 128 keys all lie in the packed rows or the pool comes by tiled copies, one
+  // per page and 64 columns; others (a sequence's last, staged rows, pages that
+  // no box fits) row by row, with zeros for rows past the keys, so what lies
+  // there cannot reach a product.
   __device__ bool load_kv(const AttendPiece& p, int t, int v) {
     if (!wait_bar(&sh->kv_empty[kv.i], kv.ph ^ 1, sh, a.status)) return false;
     const uint32_t tile = tiles + (2 + kv.i) * Tile<DP>::kBytes;
+    const int pooled = a.stage_k ? p.s.len - p.s.n : p.s.len;
+    if (a.box_rows && (t + 1) * kTileKeys <= pooled) {
+      if (lt < 32) load_boxes(p, t, v, tile);
+      if (lt != 0) mbar_arrive(&sh->kv_full[kv.i]);
+    } else {
+      load_rows(p, t, v, tile, pooled);
+      cp_async_arrive(&sh->kv_full[kv.i]);
+    }
+    kv.step();
+    ++issued;
+    return true;
+  }
+  // One warp: lane 0 announces the bytes, a lane per page copies.
+  __device__ void load_boxes(const AttendPiece& p, int t, int v, uint32_t tile) {
+    uint64_t* bar = &sh->kv_full[kv.i];
+    const void* map = v ? &a.map_v : &a.map_k;
+    const int key0 = t * kTileKeys;
+    const int halves = a.dim > 64 ? 2 : 1;
+    if (lt == 0) mbar_arrive_expect_tx(bar, halves * (128 * 128));
+    __syncwarp();
+    if (!a.tables) {
+      if (lt < halves) tma_box3(tile + lt * (128 * 128), map, lt * 64, p.h, p.s.row0 + key0, bar);
+      return;
+    }
+    if (lt * a.box_rows >= kTileKeys) return;
+    const int key = key0 + lt * a.box_rows, blk = key / a.block_size;
+    int id = a.tables[(long long)p.b * a.max_blocks + blk];
+    if (id < 0 || id >= a.num_blocks) {
+      set_status(a.status, SPEC_EDEVICE);
+      id = a.num_blocks;  // outside the tensor: zeros
+    }
+    for (int i = 0; i < halves; ++i)
+      tma_box4(tile + i * (128 * 128) + lt * a.box_rows * 128, map, i * 64, p.h,
+               key - blk * a.block_size, id, bar);
+  }
+  __device__ void load_rows(const AttendPiece& p, int t, int v, uint32_t tile, int pooled) {
     const int c = lt % kChunks;
     const long long col = ((long long)p.h * a.dim + c * 8) * 2;
     const unsigned char* base = v ? a.v : a.k;
     const long long ld = v ? a.ld_v : a.ld_k;
-    const int pooled = a.stage_k ? p.s.len - p.s.n : p.s.len;
     const int32_t* table = a.tables ? a.tables + (long long)p.b * a.max_blocks : nullptr;
-#pragma unroll 4
+    bool bad = false;
+#pragma unroll 8
     for (int r = lt / kChunks; r < 128; r += kRowStep) {
       const int key = t * kTileKeys + r;
       bool ok = key < p.s.len && c * 8 < a.dim;
       const unsigned char* src = base;
-      if (ok) {
-        if (!table) {
-          src = base + (p.s.row0 + key) * ld + col;
-        } else if (key < pooled) {
-          const int blk = key / a.block_size;
-          const int id = table[blk];
-          if (id < 0 || id >= a.num_blocks) {
-            ok = false;
-            set_status(a.status, SPEC_EDEVICE);
-          } else {
-            src = base + id * a.page_bytes + (key - blk * a.block_size) * ld + col;
-          }
-        } else {
-          src = (v ? a.stage_v : a.stage_k) + p.b * a.stage_seq + (key - pooled) * a.stage_row + col;
+      if (!table) {
+        src = base + (p.s.row0 + (ok ? key : 0)) * ld + col;
+      } else if (key < pooled) {
+        const int blk = key / a.block_size;
+        int id = ok ? table[blk] : 0;
+        if (id < 0 || id >= a.num_blocks) {
+          bad = true;
+          ok = false;
+          id = 0;
         }
+        src = base + id * a.page_bytes + (key - blk * a.block_size) * ld + col;
+      } else if (ok) {
+        src = (v ? a.stage_v : a.stage_k) + p.b * a.stage_seq + (key - pooled) * a.stage_row + col;
       }
       cp_async16(chunk_addr(tile, r), src, ok ? 16u : 0u);
     }
-    cp_async_arrive(&sh->kv_full[kv.i]);
-    kv.step();
-    return true;
+    if (bad) set_status(a.status, SPEC_EDEVICE);
   }
   __device__ void run(AttendShape shape) {
     Cursor cur = cursor(a, shape, sh);
@@ -297,7 +341,7 @@ struct Issuer {
   Ring<Tile<DP>::kStages> kv;
   Ring<2> q;
   uint32_t p_ph[2];
-  uint32_t pieces;
+  uint32_t pieces;  // with K/V tiles
 
   __device__ bool wait(uint64_t* bar, uint32_t ph) { return wait_bar(bar, ph, sh, a.status); }
   // The next K or V tile in shared memory (its address in *addr).
@@ -336,18 +380,17 @@ struct Issuer {
   __device__ bool piece(const AttendShape& shape, const AttendPiece& p) {
     const int m = p.t1 - p.t0;
     const bool two = p.ntok > shape.tpt;
+    if (m == 0) return true;  // rows that see nothing
     uint32_t qa[2], ka, va;
     int qs[2];
-    if (m > 0) {
-      for (int w = 0; w < (two ? 2 : 1); ++w) {
-        if (!wait(&sh->q_full[q.i], q.ph)) return false;
-        fence_proxy_async_smem();
-        qa[w] = tiles + q.i * Tile<DP>::kBytes;
-        qs[w] = q.i;
-        q.step();
-      }
+    for (int w = 0; w < (two ? 2 : 1); ++w) {
+      if (!wait(&sh->q_full[q.i], q.ph)) return false;
+      fence_proxy_async_smem();
+      qa[w] = tiles + q.i * Tile<DP>::kBytes;
+      qs[w] = q.i;
+      q.step();
     }
-    if (m > 0 && two) {
+    if (two) {
       const int c0 = first_tile_count(shape, p);
       if (!acquire(&ka)) return false;
       if (c0 > 0) qk(0, qa[0], ka);
@@ -355,7 +398,7 @@ struct Issuer {
       qk(1, qa[1], ka);
       release();
       if (m == 1) tc_commit(&sh->q_empty[qs[1]]);
-    } else if (m > 0) {
+    } else {
       for (int i = 0; i < min(2, m); ++i) {
         if (!acquire(&ka)) return false;
         qk(i, qa[0], ka);
@@ -367,7 +410,6 @@ struct Issuer {
     if (pieces > 0 && !wait(&sh->o_empty, (pieces - 1) & 1)) return false;
     ++pieces;
     tc_fence_after();
-    if (m == 0) return true;
     if (two) {
       const int c0 = first_tile_count(shape, p);
       for (int i = 0; i < m; ++i) {
@@ -556,13 +598,7 @@ struct Softmax {
     Cursor cur = cursor(a, shape, sh);
     AttendPiece p;
     AttendRec rec = {};
-    bool skipped = false;  // a phase of the other accumulator's barrier not yet waited for
     while (cur.next(&p)) {
-      if (skipped) {
-        if (!wait(&sh->o_full[w ^ 1], o_ph[w ^ 1])) return;
-        o_ph[w ^ 1] ^= 1;
-        skipped = false;
-      }
       const int m_tiles = p.t1 - p.t0;
       const bool two = p.ntok > shape.tpt;
       const int base = two ? w * shape.tpt : 0;  // the tile's first token in the unit
@@ -603,7 +639,6 @@ struct Softmax {
           if (!wait(&sh->o_full[x], o_ph[x])) return;
           o_ph[x] ^= 1;
         }
-      skipped = two && (w ? c0 : c1) > 0;
       if (!two) {  // both warpgroups hold part of every row: join, half the columns each
         sh->ml[w][row] = make_float2(m, l);
         arrive(&sh->swap);
@@ -651,7 +686,13 @@ struct Softmax {
         }
         tc_fence_before();
       }
-      arrive(&sh->o_empty);
+      // Both accumulators' phases are waited for before either is given back, so
+      // no barrier can run two phases ahead of a waiting warp.
+      if (two && (w ? c0 : c1) > 0) {
+        if (!wait(&sh->o_full[w ^ 1], o_ph[w ^ 1])) return;
+        o_ph[w ^ 1] ^= 1;
+      }
+      if (m_tiles > 0) arrive(&sh->o_empty);
     }
     if (threadIdx.x == 0) a.rec[blockIdx.x] = rec;
   }
@@ -699,9 +740,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       s.run(shape);
     }
   } else {
-    Loader<DP> s{a, sh, tiles, tid - 9 * 32, {}, {}};
+    Loader<DP> s{a, sh, tiles, tid - 9 * 32, {}, {}, 0};
     s.run(shape);
     cp_async_wait_all();
+    if (*(volatile int*)&sh->abort) s.drain();
   }
   __syncwarp();
   tc_fence_before();
@@ -779,6 +821,61 @@ cudaError_t launch(const AttendArgs& a, cudaStream_t st) {
 }
 
 }  // namespace
+
+namespace {
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      p = nullptr;
+    }
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn;
+}
+}  // namespace
+
+// Packed rows: (column, head, row), boxes of 128 rows. Pages: (column, head,
+// row, block), boxes of a whole page where its rows divide the tile, or of 128
+// rows where the tile's rows divide the page; a box begins on a whole 1024-byte
+// swizzle atom, so pages of fewer than 8 rows are left to the row copies.
+// Columns past the head's end are filled with zeros.
+void attend_maps(AttendArgs* a) {
+  a->box_rows = 0;
+  const int bs = a->block_size;
+  int rows = kTileKeys;
+  if (a->tables) {
+    if (bs % kTileKeys != 0) rows = (bs >= 8 && kTileKeys % bs == 0) ? bs : 0;
+  }
+  const EncodeFn encode = rows ? encode_fn() : nullptr;
+  if (!encode) return;
+  const cuuint32_t rank = a->tables ? 4 : 3;
+  for (int v = 0; v < 2; ++v) {
+    const cuuint64_t ld = (cuuint64_t)(v ? a->ld_v : a->ld_k);
+    const cuuint64_t dims[4] = {(cuuint64_t)a->dim, (cuuint64_t)a->kv_heads,
+                                (cuuint64_t)(a->tables ? bs : a->T), (cuuint64_t)a->num_blocks};
+    const cuuint64_t strides[3] = {(cuuint64_t)a->dim * 2, ld, (cuuint64_t)a->page_bytes};
+    const cuuint32_t box[4] = {64, 1, (cuuint32_t)rows, 1};
+    const cuuint32_t step[4] = {1, 1, 1, 1};
+    if (encode(v ? &a->map_v : &a->map_k,
+               a->dtype == SPEC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                     : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+               rank, const_cast<unsigned char*>(v ? a->v : a->k), dims, strides, box, step,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return;
+  }
+  a->box_rows = rows;
+}
 
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
   if (a.dtype == SPEC_BF16)

@@ -1,5 +1,7 @@
 // Arguments and launchers of the attention operators.
 #pragma once
+#include <cuda.h>
+
 #include "attend_plan.cuh"
 #include "common.cuh"
 
@@ -47,7 +49,13 @@ struct AttendArgs {
   float2* part_ml;   // [2 * ctas][2 * kTileRows] (maximum in log2 units, sum)
   AttendRec* rec;    // [ctas]
   int ctas;
+  // K and V as tensors (column, head, row, block) for tiled copies of box_rows
+  // rows of 64 columns each; box_rows 0: none, rows are copied one by one.
+  int box_rows;
+  CUtensorMap map_k, map_v;
 };
+// Forms the maps where the layout allows tiled copies (attend.cu says which).
+void attend_maps(AttendArgs* a);
 // Workspace bytes of the parts, for rows padded to DP columns.
 struct AttendWs {
   size_t o, ml, rec, total;

@@ -975,6 +975,7 @@ int spec_attend_prompt(const void* q, int64_t ld_q, const void* k, int64_t ld_k,
   a.v = (const unsigned char*)v;
   a.ld_k = ld_k * 2;
   a.ld_v = ld_v * 2;
+  attend_maps(&a);
   return cuda_status(launch_attend(a, (cudaStream_t)stream));
 }
 
@@ -1015,6 +1016,7 @@ int spec_attend_paged(const void* q, int64_t ld_q, int dtype, const int32_t* row
     a.stage_seq = Kp1 * a.stage_row;
     a.stage_rows = Kp1;
   }
+  attend_maps(&a);
   return cuda_status(launch_attend(a, (cudaStream_t)stream));
 }
 
