@@ -36,42 +36,50 @@ constexpr int kLoaders = 96;      // warps 9-11
 constexpr int kTmemCols = 512;    // S0 S1 O0 O1
 constexpr float kSlack = 8.0f;    // log2 of the largest p~
 
+// Buffers of one 128-row tile (Q, K or V) each; all of them serve all three.
 template <int DP>
 struct Tile {
   static constexpr int kBytes = 128 * DP * 2;
-  static constexpr int kStages = DP == 128 ? 5 : 10;
-  static constexpr int kSmemTiles = (2 + kStages) * kBytes;
+  static constexpr int kCount = DP == 128 ? 7 : 13;
+  static constexpr int kSmemTiles = kCount * kBytes;
 };
 
 struct Shared {
-  uint64_t kv_full[10], kv_empty[10];
-  uint64_t q_full[2], q_empty[2];
+  uint64_t full[13], empty[13];
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t o_empty, swap, drain;
   uint32_t tmem;
   int abort;
   long long warp_sum[kThreads / 32];
+  AttendSeq seq;      // the first unit's sequence
   int start[4];       // sequence, head, unit, cost taken of it
   long long run;      // cost of this CTA's run
   float2 ml[2][kTileRows];
 };
 static_assert(Tile<128>::kSmemTiles + sizeof(Shared) <= 227 * 1024, "shared memory");
 
-// A wait on a barrier phase, at most kWaitLimitNs; a wait that runs out (or
-// another's that did) ends the CTA's work.
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Shared* sh,
-                                         int32_t* status) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
+// A wait on a barrier phase, bounded by kWaitCycles of the SM's clock (2 s at
+// 1.9 GHz; cheaper to read than the global timer). A wait that runs out (or another's
+// that did) ends the CTA's work.
+constexpr long long kWaitCycles = 3800000000ll;
+__device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity, Shared* sh,
+                                       int32_t* status) {
+  const long long t0 = clock64();
   for (;;) {
-    if (mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
     if (*(volatile int*)&sh->abort) return false;
-    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+    if (clock64() - t0 > kWaitCycles) {
       *(volatile int*)&sh->abort = 1;
       set_status(status, SPEC_ETIMEOUT);
       return false;
     }
   }
+}
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Shared* sh,
+                                         int32_t* status) {
+  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, sh, status);
 }
 
 // Sequence b, with what is invalid made empty.
@@ -109,9 +117,15 @@ struct SeqOf {
 
 using Cursor = AttendCursor<SeqOf>;
 
+// a / b where it mostly fits 32 bits
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // Where this CTA's run of the cost line starts, into sh; all threads.
-__device__ void find_run(const AttendArgs& a, AttendShape shape, Shared* sh) {
+__device__ __forceinline__ void find_run(const AttendArgs& a, Shared* sh) {
   const SeqOf seq{&a};
+  const AttendShape& shape = a.shape;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.B + kThreads - 1) / kThreads;
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
@@ -131,27 +145,28 @@ __device__ void find_run(const AttendArgs& a, AttendShape shape, Shared* sh) {
   if (lane == 31) sh->warp_sum[warp] = incl;
   __syncthreads();
   long long before = 0, total = 0;
+#pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += sh->warp_sum[w];
     total += sh->warp_sum[w];
   }
-  const long long share = (total + gridDim.x - 1) / gridDim.x;
+  const long long share = quotient(total + gridDim.x - 1, gridDim.x);
   const long long from = share * blockIdx.x;
   const long long to = min(total, from + share);
-  if (tid == 0 && from >= to) sh->run = 0;
   long long at = before + incl - sum;
   if (from < to && from >= at && from < at + sum) {
     for (int b = b0; b < b1; ++b) {
       const AttendSeq s = seq(b);
       const long long head = shape.head_cost(s);
       if (from < at + head * a.kv_heads) {
-        const int h = (int)((from - at) / head);
+        const int h = (int)quotient(from - at, head);
         const long long y = from - at - h * head;
         int lo = 0, hi = shape.units(s) - 1;  // the unit u with cost_before(u) <= y
         while (lo < hi) {
           const int mid = (lo + hi + 1) >> 1;
           if (shape.cost_before(s, mid) <= y) lo = mid; else hi = mid - 1;
         }
+        sh->seq = s;
         sh->start[0] = b;
         sh->start[1] = h;
         sh->start[2] = lo;
@@ -165,28 +180,112 @@ __device__ void find_run(const AttendArgs& a, AttendShape shape, Shared* sh) {
   __syncthreads();
 }
 
-__device__ __forceinline__ Cursor cursor(const AttendArgs& a, AttendShape shape, const Shared* sh) {
-  return Cursor(shape, SeqOf{&a}, a.B, a.kv_heads, sh->start[0], sh->start[1], sh->start[2],
-                sh->start[3], sh->run);
+__device__ __forceinline__ Cursor cursor(const AttendArgs& a, const Shared* sh) {
+  return Cursor(a.shape, SeqOf{&a}, a.B, a.kv_heads, sh->start[0], sh->start[1], sh->start[2],
+                sh->start[3], sh->run, sh->seq);
 }
 
-// A ring position: slot and the parity of its phase.
+// The free buffers, in the order in which they will be given back: a queue of
+// 4-bit numbers, the next one lowest. The loading and the issuing warps step
+// through one program of takes and gives, so each n-th take gets the same
+// buffer on both sides; the barriers' phases follow from each buffer's uses.
 template <int N>
-struct Ring {
-  int i = 0;
-  uint32_t ph = 0;
-  __device__ void step() {
-    if (++i == N) {
-      i = 0;
-      ph ^= 1;
-    }
+struct Buffers {
+  uint64_t queue;
+  int count;
+  uint32_t phases;  // bit b: parity of buffer b's next use
+  __device__ Buffers() : queue(0), count(N), phases(0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) queue |= (uint64_t)i << (4 * i);
+  }
+  __device__ int take(uint32_t* parity) {
+    const int b = (int)(queue & 15);
+    queue >>= 4;
+    --count;
+    *parity = (phases >> b) & 1;
+    phases ^= 1u << b;
+    return b;
+  }
+  __device__ void give(int b) {
+    queue |= (uint64_t)b << (4 * count);
+    ++count;
   }
 };
+
+// One lane of a warp, the same for every call by the whole warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
 
 // Tiles of a unit that its first 128-row tile needs (two-tile units).
 __device__ __forceinline__ int first_tile_count(const AttendShape& shape, const AttendPiece& p) {
   const int nt0 = shape.tiles_upto(p.s, p.tok0 + shape.tpt - 1);
   return max(0, min(p.t1, nt0) - p.t0);
+}
+
+// The program of a piece that the loading warps (which fill what is taken)
+// and the issuing warp (which uses it) share. Side:
+//   take_q(w), take_k(t), take_v(t): the next buffer, for the query tile of
+//     warpgroup w, K or V tile t; a K tile lasts until give_k, V until give_v;
+//   qk(w), pv(w, first, last): the products; give_q(w).
+template <typename Side>
+__device__ __forceinline__ bool piece_program(const AttendShape& shape, const AttendPiece& p,
+                                              Side& side) {
+  const int m = p.t1 - p.t0;
+  if (m == 0) return true;  // rows that see nothing
+  if (p.ntok > shape.tpt) {
+    // Two query tiles share each K/V tile; the first may need fewer of them.
+    const int c0 = first_tile_count(shape, p);
+    if (!side.take_q(0) || !side.take_q(1) || !side.take_k(0)) return false;
+    if (c0 > 0) side.qk(0);
+    if (c0 <= 1) side.give_q(0);
+    side.qk(1);
+    side.give_k();
+    if (m == 1) side.give_q(1);
+    if (!side.begin_pv()) return false;
+    for (int i = 0; i < m; ++i) {
+      const bool more = i + 1 < m;
+      if (!side.take_v(i)) return false;
+      if (i < c0 && !side.pv(0, i == 0, i == c0 - 1)) return false;
+      if (more) {
+        if (!side.take_k(i + 1)) return false;
+        if (i + 1 < c0) side.qk(0);
+        if (i + 1 == c0 - 1) side.give_q(0);
+      }
+      if (!side.pv(1, i == 0, !more)) return false;
+      side.give_v();
+      if (more) {
+        side.qk(1);
+        side.give_k();
+        if (i + 2 == m) side.give_q(1);
+      }
+    }
+  } else {
+    // One query tile; the K/V tiles go to the two accumulators in turn.
+    if (!side.take_q(0)) return false;
+    for (int i = 0; i < min(2, m); ++i) {
+      if (!side.take_k(i)) return false;
+      side.qk(i);
+      side.give_k();
+    }
+    if (m <= 2) side.give_q(0);
+    if (!side.begin_pv()) return false;
+    for (int i = 0; i < m; ++i) {
+      if (!side.take_v(i) || !side.pv(i & 1, i < 2, i + 2 >= m)) return false;
+      side.give_v();
+      if (i + 2 < m) {
+        if (!side.take_k(i + 2)) return false;
+        side.qk(i & 1);
+        side.give_k();
+        if (i + 3 == m) side.give_q(0);
+      }
+    }
+  }
+  return true;
 }
 
 // ---------------------------------------------------------------------------
@@ -200,84 +299,122 @@ struct Loader {
   Shared* sh;
   uint32_t tiles;   // shared address of the tiles
   int lt;           // 0 .. 95
-  Ring<Tile<DP>::kStages> kv;
-  Ring<2> q;
-  uint32_t issued;
+  Buffers<Tile<DP>::kCount> buf;
+  AttendPiece p;
+  int q_buf[2], k_buf, v_buf;
+  uint32_t issued;  // buffers filled at least once, by bit
+  // Table entries of 32 consecutive pages, one per lane: the group that the K
+  // tiles have reached, the one before (V tiles follow) and the next one.
+  int group, cur, prev, next;
 
+  __device__ Loader(const AttendArgs& a_, Shared* s, uint32_t t, int l)
+      : a(a_), sh(s), tiles(t), lt(l), issued(0) {}
+  __device__ bool wait(uint64_t* bar, uint32_t ph) {
+    return __all_sync(0xffffffffu, wait_bar(bar, ph, sh, a.status));
+  }
   // After a wait that ran out: the copies in flight land before the CTA ends.
   __device__ void drain() {
-    for (uint32_t j = 0; j < Tile<DP>::kStages && j < issued; ++j) {
-      const uint32_t n = issued - 1 - j;
-      mbar_wait_bounded(&sh->kv_full[n % Tile<DP>::kStages], (n / Tile<DP>::kStages) & 1,
-                        kWaitLimitNs);
-    }
+    for (int b = 0; b < Tile<DP>::kCount; ++b)
+      if (issued >> b & 1)
+        mbar_wait_bounded(&sh->full[b], ((buf.phases >> b) & 1) ^ 1, kWaitLimitNs);
   }
+  __device__ bool take(int* b) {
+    uint32_t ph;
+    *b = buf.take(&ph);
+    if (!wait(&sh->empty[*b], ph ^ 1)) {
+      buf.phases ^= 1u << *b;  // not filled
+      return false;
+    }
+    issued |= 1u << *b;
+    return true;
+  }
+  __device__ uint32_t tile(int b) const { return tiles + b * Tile<DP>::kBytes; }
   __device__ uint32_t chunk_addr(uint32_t tile, int row) const {
     const int c = lt % kChunks;
     return tile + (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
   }
-  __device__ bool load_q(const AttendPiece& p, int tok0, int ntok, int tpt) {
-    if (!wait_bar(&sh->q_empty[q.i], q.ph ^ 1, sh, a.status)) return false;
-    const uint32_t tile = tiles + q.i * Tile<DP>::kBytes;
-    const int c = lt % kChunks;
-    const int rows = min(ntok, tpt) * a.group;
+  __device__ int entry(int page) const {
+    return page < a.max_blocks ? a.tables[(long long)p.b * a.max_blocks + page] : 0;
+  }
+  __device__ int first_page(int t) const { return (int)a.by_bs((uint32_t)(t * kTileKeys)); }
+  __device__ void begin() {
+    if (!a.tables || !a.box_rows || p.t1 == p.t0) return;
+    group = first_page(p.t0) >> 5;
+    cur = entry(group * 32 + (lt & 31));
+    next = entry(group * 32 + 32 + (lt & 31));
+    prev = 0;
+  }
+  __device__ bool take_q(int w) {
+    if (!take(&q_buf[w])) return false;
+    const uint32_t dst = tile(q_buf[w]);
+    const int c = lt % kChunks, tpt = a.shape.tpt;
+    const int tok0 = p.tok0 + w * tpt, rows = min(p.ntok - w * tpt, tpt) * a.group;
+    const unsigned char* base =
+        a.q + (long long)(p.s.row0 + tok0) * a.ld_q + ((long long)p.h * a.group * a.dim + c * 8) * 2;
+#pragma unroll 4
     for (int r = lt / kChunks; r < 128; r += kRowStep) {
-      const int t = r / a.group, g = r - t * a.group;
+      const int t = (int)a.by_group((uint32_t)r), g = r - t * a.group;
       const bool ok = r < rows && c * 8 < a.dim;
-      const unsigned char* src =
-          a.q + (ok ? (p.s.row0 + tok0 + t) * a.ld_q +
-                          ((long long)(p.h * a.group + g) * a.dim + c * 8) * 2
-                    : 0);
-      cp_async16(chunk_addr(tile, r), src, ok ? 16u : 0u);
+      const unsigned char* src = ok ? base + t * a.ld_q + g * a.dim * 2 : a.q;
+      cp_async16(chunk_addr(dst, r), src, ok ? 16u : 0u);
     }
-    cp_async_arrive(&sh->q_full[q.i]);
-    q.step();
+    cp_async_arrive(&sh->full[q_buf[w]]);
     return true;
   }
-  // K (v = 0) or V (v = 1) rows of tile t of piece p's sequence. A tile whose
+  __device__ bool take_k(int i) { return take(&k_buf) && load_kv(p.t0 + i, 0, k_buf); }
+  __device__ bool take_v(int i) { return take(&v_buf) && load_kv(p.t0 + i, 1, v_buf); }
+  // K (v = 0) or V (v = 1) rows of tile t of the piece's sequence. A tile whose
   // 128 keys all lie in the packed rows or the pool comes by tiled copies, one
   // per page and 64 columns; others (a sequence's last, staged rows, pages that
   // no box fits) row by row, with zeros for rows past the keys, so what lies
   // there cannot reach a product.
-  __device__ bool load_kv(const AttendPiece& p, int t, int v) {
-    if (!wait_bar(&sh->kv_empty[kv.i], kv.ph ^ 1, sh, a.status)) return false;
-    const uint32_t tile = tiles + (2 + kv.i) * Tile<DP>::kBytes;
+  __device__ bool load_kv(int t, int v, int b) {
     const int pooled = a.stage_k ? p.s.len - p.s.n : p.s.len;
     if (a.box_rows && (t + 1) * kTileKeys <= pooled) {
-      if (lt < 32) load_boxes(p, t, v, tile);
-      if (lt != 0) mbar_arrive(&sh->kv_full[kv.i]);
+      load_boxes(t, v, tile(b), &sh->full[b]);
     } else {
-      load_rows(p, t, v, tile, pooled);
-      cp_async_arrive(&sh->kv_full[kv.i]);
+      load_rows(t, v, tile(b), pooled);
+      cp_async_arrive(&sh->full[b]);
     }
-    kv.step();
-    ++issued;
     return true;
   }
-  // One warp: lane 0 announces the bytes, a lane per page copies.
-  __device__ void load_boxes(const AttendPiece& p, int t, int v, uint32_t tile) {
-    uint64_t* bar = &sh->kv_full[kv.i];
+  // 64 columns per warp; one lane announces the bytes and issues the copies.
+  __device__ void load_boxes(int t, int v, uint32_t dst, uint64_t* bar) {
+    const int half = lt >> 5, lane = lt & 31;
+    const bool mine = half * 64 < a.dim && half < 2;
+    const bool one = elect_one();
+    if (!mine || !one) mbar_arrive(bar);
+    if (!mine) return;
     const void* map = v ? &a.map_v : &a.map_k;
-    const int key0 = t * kTileKeys;
-    const int halves = a.dim > 64 ? 2 : 1;
-    if (lt == 0) mbar_arrive_expect_tx(bar, halves * (128 * 128));
-    __syncwarp();
+    dst += half * (128 * 128);
+    if (one) mbar_arrive_expect_tx(bar, 128 * 128);
     if (!a.tables) {
-      if (lt < halves) tma_box3(tile + lt * (128 * 128), map, lt * 64, p.h, p.s.row0 + key0, bar);
+      if (one) tma_box3(dst, map, half * 64, p.h, p.s.row0 + t * kTileKeys, bar);
       return;
     }
-    if (lt * a.box_rows >= kTileKeys) return;
-    const int key = key0 + lt * a.box_rows, blk = key / a.block_size;
-    int id = a.tables[(long long)p.b * a.max_blocks + blk];
+    const int page = first_page(t), g = page >> 5;
+    if (!v && g != group) {
+      prev = cur;
+      cur = next;
+      group = g;
+      next = entry(g * 32 + 32 + lane);
+    }
+    int id = g == group ? cur : prev;
+    const int row = t * kTileKeys - page * a.block_size;  // of the first page, if it is larger than a tile
+    const int boxes = kTileKeys / a.box_rows;
+    const bool used = (unsigned)(lane - (page & 31)) < (unsigned)boxes;
     if (id < 0 || id >= a.num_blocks) {
-      set_status(a.status, SPEC_EDEVICE);
+      if (used) set_status(a.status, SPEC_EDEVICE);
       id = a.num_blocks;  // outside the tensor: zeros
     }
-    for (int i = 0; i < halves; ++i)
-      tma_box4(tile + i * (128 * 128) + lt * a.box_rows * 128, map, i * 64, p.h,
-               key - blk * a.block_size, id, bar);
+#pragma unroll 4
+    for (int i = 0; i < boxes; ++i) {
+      const int from = __shfl_sync(0xffffffffu, id, (page & 31) + i);
+      if (one)
+        tma_box4(dst + i * a.box_rows * 128, map, half * 64, p.h, row, from, bar);
+    }
   }
-  __device__ void load_rows(const AttendPiece& p, int t, int v, uint32_t tile, int pooled) {
+  __device__ void load_rows(int t, int v, uint32_t dst, int pooled) {
     const int c = lt % kChunks;
     const long long col = ((long long)p.h * a.dim + c * 8) * 2;
     const unsigned char* base = v ? a.v : a.k;
@@ -292,7 +429,7 @@ struct Loader {
       if (!table) {
         src = base + (p.s.row0 + (ok ? key : 0)) * ld + col;
       } else if (key < pooled) {
-        const int blk = key / a.block_size;
+        const int blk = (int)a.by_bs((uint32_t)key);
         int id = ok ? table[blk] : 0;
         if (id < 0 || id >= a.num_blocks) {
           bad = true;
@@ -303,32 +440,27 @@ struct Loader {
       } else if (ok) {
         src = (v ? a.stage_v : a.stage_k) + p.b * a.stage_seq + (key - pooled) * a.stage_row + col;
       }
-      cp_async16(chunk_addr(tile, r), src, ok ? 16u : 0u);
+      cp_async16(chunk_addr(dst, r), src, ok ? 16u : 0u);
     }
     if (bad) set_status(a.status, SPEC_EDEVICE);
   }
-  __device__ void run(AttendShape shape) {
-    Cursor cur = cursor(a, shape, sh);
-    AttendPiece p;
-    while (cur.next(&p)) {
-      const int m = p.t1 - p.t0;
-      if (m == 0) continue;
-      const bool two = p.ntok > shape.tpt;
-      if (!load_q(p, p.tok0, p.ntok, shape.tpt)) return;
-      if (two && !load_q(p, p.tok0 + shape.tpt, p.ntok - shape.tpt, shape.tpt)) return;
-      const int ahead = two ? 1 : 2;  // K tiles used before the first V tile
-      for (int i = 0; i < min(ahead, m); ++i)
-        if (!load_kv(p, p.t0 + i, 0)) return;
-      for (int i = 0; i < m; ++i) {
-        if (!load_kv(p, p.t0 + i, 1)) return;
-        if (i + ahead < m && !load_kv(p, p.t0 + i + ahead, 0)) return;
-      }
+  __device__ void give_q(int w) { buf.give(q_buf[w]); }
+  __device__ void give_k() { buf.give(k_buf); }
+  __device__ void give_v() { buf.give(v_buf); }
+  __device__ void qk(int) {}
+  __device__ bool pv(int, bool, bool) { return true; }
+  __device__ bool begin_pv() { return true; }
+  __device__ void run() {
+    Cursor cur_ = cursor(a, sh);
+    while (cur_.next(&p)) {
+      begin();
+      if (!piece_program(a.shape, p, *this)) return;
     }
   }
 };
 
 // ---------------------------------------------------------------------------
-// Matrix instructions, issued by one thread
+// Matrix instructions, issued by one lane of a warp
 // ---------------------------------------------------------------------------
 template <typename T, int DP>
 struct Issuer {
@@ -338,129 +470,85 @@ struct Issuer {
   const AttendArgs& a;
   Shared* sh;
   uint32_t tiles, tmem;
-  Ring<Tile<DP>::kStages> kv;
-  Ring<2> q;
-  uint32_t p_ph[2];
-  uint32_t pieces;  // with K/V tiles
+  Buffers<Tile<DP>::kCount> buf;
+  int q_buf[2], k_buf, v_buf;
+  uint32_t p_ph;     // bit w: parity of p_full[w]
+  uint32_t pieces;   // with K/V tiles
 
-  __device__ bool wait(uint64_t* bar, uint32_t ph) { return wait_bar(bar, ph, sh, a.status); }
-  // The next K or V tile in shared memory (its address in *addr).
-  __device__ bool acquire(uint32_t* addr) {
-    if (!wait(&sh->kv_full[kv.i], kv.ph)) return false;
+  __device__ Issuer(const AttendArgs& a_, Shared* s, uint32_t t, uint32_t m)
+      : a(a_), sh(s), tiles(t), tmem(m), p_ph(0), pieces(0) {}
+  __device__ bool wait(uint64_t* bar, uint32_t ph) {
+    return __all_sync(0xffffffffu, wait_bar(bar, ph, sh, a.status));
+  }
+  __device__ bool take(int* b) {
+    uint32_t ph;
+    *b = buf.take(&ph);
+    if (!wait(&sh->full[*b], ph)) return false;
     fence_proxy_async_smem();
-    *addr = tiles + (2 + kv.i) * Tile<DP>::kBytes;
     return true;
   }
-  __device__ void release() {
-    tc_commit(&sh->kv_empty[kv.i]);
-    kv.step();
+  __device__ bool take_q(int w) { return take(&q_buf[w]); }
+  __device__ bool take_k(int) { return take(&k_buf); }
+  __device__ bool take_v(int) { return take(&v_buf); }
+  __device__ void give(int b) {
+    if (elect_one()) tc_commit(&sh->empty[b]);
+    buf.give(b);
   }
-  __device__ uint32_t s_col(int w) const { return tmem + w * 128; }
-  __device__ uint32_t o_col(int w) const { return tmem + 256 + w * DP; }
+  __device__ void give_q(int w) { give(q_buf[w]); }
+  __device__ void give_k() { give(k_buf); }
+  __device__ void give_v() { give(v_buf); }
+  // Low words of the descriptors; the high word is the same for all.
+  __device__ uint32_t desc(int b, uint32_t lead_bytes) const {
+    return ((tiles + b * Tile<DP>::kBytes) >> 4) | ((lead_bytes >> 4) << 16);
+  }
   // S_w = Q K^T
-  __device__ void qk(int w, uint32_t qaddr, uint32_t kaddr) {
+  __device__ void qk(int w) {
+    const uint32_t qd = desc(w && q2 ? q_buf[1] : q_buf[0], 16), kd = desc(k_buf, 16);
+    const uint32_t s = tmem + w * 128;
+    if (elect_one()) {
 #pragma unroll
-    for (int k = 0; k < DP / 16; ++k) {
-      const uint32_t off = (k >> 2) * (128 * 128) + (k & 3) * 32;
-      mma_ss(s_col(w), mma_sdesc(qaddr + off, 16), mma_sdesc(kaddr + off, 16), kIdescQK, k > 0);
-    }
-    tc_commit(&sh->s_full[w]);
-  }
-  // O_w (+)= P_w V
-  __device__ bool pv(int w, uint32_t vaddr, bool acc) {
-    if (!wait(&sh->p_full[w], p_ph[w])) return false;
-    p_ph[w] ^= 1;
-    tc_fence_after();
-#pragma unroll
-    for (int k = 0; k < kTileKeys / 16; ++k)
-      mma_ts(o_col(w), s_col(w) + k * 8, mma_sdesc(vaddr + k * (16 * 128), 128 * 128), kIdescPV,
-             acc || k > 0);
-    return true;
-  }
-  __device__ bool piece(const AttendShape& shape, const AttendPiece& p) {
-    const int m = p.t1 - p.t0;
-    const bool two = p.ntok > shape.tpt;
-    if (m == 0) return true;  // rows that see nothing
-    uint32_t qa[2], ka, va;
-    int qs[2];
-    for (int w = 0; w < (two ? 2 : 1); ++w) {
-      if (!wait(&sh->q_full[q.i], q.ph)) return false;
-      fence_proxy_async_smem();
-      qa[w] = tiles + q.i * Tile<DP>::kBytes;
-      qs[w] = q.i;
-      q.step();
-    }
-    if (two) {
-      const int c0 = first_tile_count(shape, p);
-      if (!acquire(&ka)) return false;
-      if (c0 > 0) qk(0, qa[0], ka);
-      if (c0 <= 1) tc_commit(&sh->q_empty[qs[0]]);
-      qk(1, qa[1], ka);
-      release();
-      if (m == 1) tc_commit(&sh->q_empty[qs[1]]);
-    } else {
-      for (int i = 0; i < min(2, m); ++i) {
-        if (!acquire(&ka)) return false;
-        qk(i, qa[0], ka);
-        release();
+      for (int k = 0; k < DP / 16; ++k) {
+        const uint32_t off = (k >> 2) * (128 * 128 / 16) + (k & 3) * 2;
+        mma_ss(s, mma_sdesc(qd + off), mma_sdesc(kd + off), kIdescQK, k > 0);
       }
-      if (m <= 2) tc_commit(&sh->q_empty[qs[0]]);
+      tc_commit(&sh->s_full[w]);
     }
-    // The accumulators are free once the softmax warps have read the last piece's.
+  }
+  bool q2;  // the piece has two query tiles
+  // The accumulators are free once the softmax warps have read the last piece's.
+  __device__ bool begin_pv() {
     if (pieces > 0 && !wait(&sh->o_empty, (pieces - 1) & 1)) return false;
     ++pieces;
     tc_fence_after();
-    if (two) {
-      const int c0 = first_tile_count(shape, p);
-      for (int i = 0; i < m; ++i) {
-        if (!acquire(&va)) return false;
-        const int vstage = kv.i;
-        kv.step();
-        if (i < c0) {
-          if (!pv(0, va, i > 0)) return false;
-          if (i == c0 - 1) tc_commit(&sh->o_full[0]);
-        }
-        if (i + 1 < m) {
-          if (!acquire(&ka)) return false;
-          if (i + 1 < c0) qk(0, qa[0], ka);
-          if (i + 1 == c0 - 1) tc_commit(&sh->q_empty[qs[0]]);
-        }
-        if (!pv(1, va, i > 0)) return false;
-        tc_commit(&sh->kv_empty[vstage]);
-        if (i == m - 1) tc_commit(&sh->o_full[1]);
-        if (i + 1 < m) {
-          qk(1, qa[1], ka);
-          release();
-          if (i + 1 == m - 1) tc_commit(&sh->q_empty[qs[1]]);
-        }
-      }
-    } else {
-      for (int i = 0; i < m; ++i) {
-        const int w = i & 1;
-        if (!acquire(&va)) return false;
-        if (!pv(w, va, i > 1)) return false;
-        if (i + 2 >= m) tc_commit(&sh->o_full[w]);
-        release();
-        if (i + 2 < m) {
-          if (!acquire(&ka)) return false;
-          qk(w, qa[0], ka);
-          release();
-          if (i + 2 == m - 1) tc_commit(&sh->q_empty[qs[0]]);
-        }
-      }
+    return true;
+  }
+  // O_w (+)= P_w V
+  __device__ bool pv(int w, bool first, bool last) {
+    if (!wait(&sh->p_full[w], (p_ph >> w) & 1)) return false;
+    p_ph ^= 1u << w;
+    tc_fence_after();
+    const uint32_t vd = desc(v_buf, 128 * 128);
+    const uint32_t s = tmem + w * 128, o = tmem + 256 + w * DP;
+    if (elect_one()) {
+#pragma unroll
+      for (int k = 0; k < kTileKeys / 16; ++k)
+        mma_ts(o, s + k * 8, mma_sdesc(vd + k * (16 * 128 / 16)), kIdescPV, k > 0 || !first);
+      if (last) tc_commit(&sh->o_full[w]);
     }
     return true;
   }
-  __device__ void run(AttendShape shape) {
-    Cursor cur = cursor(a, shape, sh);
+  __device__ void run() {
+    Cursor cur = cursor(a, sh);
     AttendPiece p;
-    while (cur.next(&p))
-      if (!piece(shape, p)) {
+    while (cur.next(&p)) {
+      q2 = p.ntok > a.shape.tpt;
+      if (!piece_program(a.shape, p, *this)) {
         // Instructions in flight end before tensor memory is given back.
-        tc_commit(&sh->drain);
+        if (elect_one()) tc_commit(&sh->drain);
         mbar_wait_bounded(&sh->drain, 0, kWaitLimitNs);
         return;
       }
+    }
   }
 };
 
@@ -482,6 +570,26 @@ template <> struct Pack<__half> {
     return r;
   }
 };
+
+// Two fp32 operations per instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
 __device__ __forceinline__ float weight(float m, float ref) {
   return m == -INFINITY ? 0.0f : ex2(m - ref);
@@ -525,7 +633,12 @@ struct Softmax {
 #pragma unroll
       for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(s[i]);
 #pragma unroll
-      for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
+      for (int i = 4; i < 124; i += 8)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          mx[j] = fmaxf(fmaxf(mx[j], __uint_as_float(s[i + j])), __uint_as_float(s[i + 4 + j]));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], __uint_as_float(s[124 + j]));
       const float top =
           fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
       const bool raise = top > m + kSlack || (m == -INFINITY && top > m);
@@ -546,21 +659,26 @@ struct Softmax {
         }
       }
       const float ref = m == -INFINITY ? 0.0f : m;
-      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      const uint64_t c2 = pair(a.scale_log2, a.scale_log2), r2 = pair(-ref, -ref);
+      uint64_t sum[2] = {0, 0};
 #pragma unroll
       for (int i = 0; i < 128; i += 64) {
         uint32_t p[32];
 #pragma unroll
         for (int j = 0; j < 64; j += 2) {
-          const float e0 = ex2(fmaf(__uint_as_float(s[i + j]), a.scale_log2, -ref));
-          const float e1 = ex2(fmaf(__uint_as_float(s[i + j + 1]), a.scale_log2, -ref));
-          sum[j & 2] += e0;
-          sum[(j & 2) + 1] += e1;
+          float e0, e1;
+          unpair(fma2(pair(__uint_as_float(s[i + j]), __uint_as_float(s[i + j + 1])), c2, r2), e0,
+                 e1);
+          e0 = ex2(e0);
+          e1 = ex2(e1);
+          sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], pair(e0, e1));
           p[j / 2] = Pack<T>::two(e0, e1);
         }
         tmem_st32(col + i / 2, p, 0);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      float l0, l1;
+      unpair(add2(sum[0], sum[1]), l0, l1);
+      l += l0 + l1;
       tmem_wait_st();
       tc_fence_before();
     }
@@ -594,8 +712,9 @@ struct Softmax {
             make_uint4(Pack<T>::two(o[i], o[i + 1]), Pack<T>::two(o[i + 2], o[i + 3]),
                        Pack<T>::two(o[i + 4], o[i + 5]), Pack<T>::two(o[i + 6], o[i + 7]));
   }
-  __device__ void run(AttendShape shape) {
-    Cursor cur = cursor(a, shape, sh);
+  __device__ void run() {
+    const AttendShape& shape = a.shape;
+    Cursor cur = cursor(a, sh);
     AttendPiece p;
     AttendRec rec = {};
     while (cur.next(&p)) {
@@ -704,13 +823,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   Shared* sh = reinterpret_cast<Shared*>(smem + Tile<DP>::kSmemTiles);
   const int tid = threadIdx.x, warp = tid >> 5;
   if (tid == 0) {
-    for (int i = 0; i < Tile<DP>::kStages; ++i) {
-      mbar_init(&sh->kv_full[i], kLoaders);
-      mbar_init(&sh->kv_empty[i], 1);
+    for (int i = 0; i < Tile<DP>::kCount; ++i) {
+      mbar_init(&sh->full[i], kLoaders);
+      mbar_init(&sh->empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh->q_full[i], kLoaders);
-      mbar_init(&sh->q_empty[i], 1);
       mbar_init(&sh->s_full[i], 1);
       mbar_init(&sh->p_full[i], 4);
       mbar_init(&sh->o_full[i], 1);
@@ -724,24 +841,26 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   }
   pdl_begin();
   if (warp == 8) tmem_alloc(&sh->tmem, kTmemCols);
-  const AttendShape shape{kTileRows / a.group};
   tc_fence_before();
-  find_run(a, shape, sh);  // its barriers publish the above
+  find_run(a, sh);  // its barriers publish the above
   tc_fence_after();
   const uint32_t tiles = smem_u32(smem), tmem = sh->tmem;
+  // Of the 384 * 168 registers of the launch, 208 to each softmax thread (a row's
+  // 128 scores and their weights stay in registers), 88 to the others.
   if (warp < 8) {
-    const int row = tid & 127;
-    Softmax<T, DP> s{a, sh, tmem + ((uint32_t)(warp & 3) << 21), warp >> 2, row, row / a.group,
-                     row % a.group, 0, {0, 0}, 0};
-    s.run(shape);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int row = tid & 127, t = (int)a.by_group((uint32_t)row);
+    Softmax<T, DP> s{a, sh, tmem + ((uint32_t)(warp & 3) << 21), warp >> 2, row, t,
+                     row - t * a.group, 0, {0, 0}, 0};
+    s.run();
   } else if (warp == 8) {
-    if ((tid & 31) == 0) {
-      Issuer<T, DP> s{a, sh, tiles, tmem, {}, {}, {0, 0}, 0};
-      s.run(shape);
-    }
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    Issuer<T, DP> s(a, sh, tiles, tmem);
+    s.run();
   } else {
-    Loader<DP> s{a, sh, tiles, tid - 9 * 32, {}, {}, 0};
-    s.run(shape);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    Loader<DP> s(a, sh, tiles, tid - 9 * 32);
+    s.run();
     cp_async_wait_all();
     if (*(volatile int*)&sh->abort) s.drain();
   }
@@ -769,7 +888,7 @@ __global__ void __launch_bounds__(kCombineThreads) attend_combine_kernel(const _
   if (!rec.head) return;
   int last = min(c + 1, a.ctas - 1);  // CTAs c .. last hold the unit's parts
   while (last + 1 < a.ctas && a.rec[last].first && a.rec[last].first_cont) ++last;
-  const int tpt = kTileRows / a.group;
+  const int tpt = a.shape.tpt;
   const bool two = rec.ntok > tpt;
   const int lane = threadIdx.x & 31;
   constexpr int kCols = DP / 32;

@@ -23,6 +23,8 @@ struct AttendRec {
 struct AttendArgs {
   int B, T, q_heads, kv_heads, group, dim;
   int dtype;          // SPEC_BF16 or SPEC_F16
+  AttendShape shape;
+  FastDiv by_group, by_bs;  // division by group, block_size
   int rows_per_seq;   // rows of each sequence where row_off is NULL
   const int32_t* row_off;
   float scale_log2;   // scale * log2(e)

@@ -53,41 +53,83 @@ struct AttendSeq {
   int row0, n, len;
 };
 
+// Division by a fixed d >= 1 of n < 2^31: n / d = (n * mul) >> (31 + bits), bits =
+// ceil(log2 d), mul = floor(2^(31+bits) / d) + 1 < 2^32 (Granlund and Montgomery,
+// "Division by invariant integers using multiplication", PLDI 1994).
+struct FastDiv {
+  uint32_t d, mul;
+  int bits;
+  SPECV_HD uint32_t operator()(uint32_t n) const {
+    return (uint32_t)(((unsigned long long)n * mul) >> (31 + bits));
+  }
+};
+inline FastDiv fast_div(uint32_t d) {
+  FastDiv f{d, 0, 0};
+  while ((1u << f.bits) < d) ++f.bits;
+  f.mul = (uint32_t)((1ull << (31 + f.bits)) / d + 1);
+  return f;
+}
+
 struct AttendShape {
-  int tpt;  // tokens of a tile
-  SPECV_HD int units(const AttendSeq& s) const { return (s.n + 2 * tpt - 1) / (2 * tpt); }
+  int tpt;     // tokens of a tile
+  int w;       // tokens of a unit, 2 * tpt
+  int log_w;   // log2 of w, -1 where it is no power of two
+  FastDiv by_w;
+
+  SPECV_HD int units(const AttendSeq& s) const { return (int)by_w((uint32_t)(s.n + w - 1)); }
   // K/V tiles that rows up to token `last` need.
   SPECV_HD int tiles_upto(const AttendSeq& s, int last) const {
     const int key = s.len - s.n + last;
     return key < 0 ? 0 : key / kTileKeys + 1;
   }
   SPECV_HD int unit_tiles(const AttendSeq& s, int u) const {
-    const int end = (u + 1) * 2 * tpt;
+    const int end = (u + 1) * w;
     return tiles_upto(s, (end < s.n ? end : s.n) - 1);
+  }
+  // sum_{j<x} floor(j / 2^r)
+  SPECV_HD static long long step_sum(long long x, int r) {
+    const long long t = x >> r;
+    return ((t * (t - 1) / 2) << r) + t * (x - (t << r));
+  }
+  // sum_{i<m} floor((b + i*w) / 128), b >= 0: closed where w is a power of two.
+  SPECV_HD long long tile_sum(long long m, int b) const {
+    if (log_w < 0) return floor_sum(m, kTileKeys, w, b);
+    if (log_w >= 7) return m * (b >> 7) + (m * (m - 1) / 2 << (log_w - 7));
+    const int s = (b & 127) >> log_w;  // floor((b + i*w) / 128) = b>>7 + floor((s + i) / (128/w))
+    return m * (b >> 7) + step_sum(m + s, 7 - log_w) - step_sum(s, 7 - log_w);
   }
   // Cost of units 0 .. u-1.
   SPECV_HD long long cost_before(const AttendSeq& s, int u) const {
     const int all = units(s);
     long long c = (long long)u * kUnitCost;
-    int full = u;  // units whose last token is (i + 1) * 2 * tpt - 1
+    int full = u;  // units whose last token is (i + 1) * w - 1
     if (u == all && u > 0) {
       c += unit_tiles(s, u - 1);
       --full;
     }
     // sum_{i=1}^{full} of floor((base + i*w - 1) / 128) + 1 where that is >= 0
-    const int w = 2 * tpt, base = s.len - s.n;
+    const int base = s.len - s.n;
     int skip = 0;  // units whose rows see nothing
     if (base < 0) {
       skip = (-base) / w;  // base + i*w - 1 < 0 for i <= skip
       if (skip > full) skip = full;
     }
     const long long m = full - skip;
-    if (m > 0)
-      c += m + floor_sum(m, kTileKeys, w, (long long)base + (long long)(skip + 1) * w - 1);
+    if (m > 0) c += m + tile_sum(m, base + (skip + 1) * w - 1);
     return c;
   }
   SPECV_HD long long head_cost(const AttendSeq& s) const { return cost_before(s, units(s)); }
 };
+inline AttendShape attend_shape(int group) {
+  AttendShape s;
+  s.tpt = kTileRows / group;
+  s.w = 2 * s.tpt;
+  s.log_w = -1;
+  for (int i = 1; i <= 8; ++i)
+    if (s.w == 1 << i) s.log_w = i;
+  s.by_w = fast_div((uint32_t)s.w);
+  return s;
+}
 
 // A CTA's share of one unit: K/V tiles [t0, t1) of the unit's nt.
 struct AttendPiece {
@@ -100,7 +142,7 @@ struct AttendPiece {
 // Walks a CTA's run of the cost line. `seq(b)` gives sequence b.
 template <typename SeqFn>
 struct AttendCursor {
-  AttendShape sh;
+  const AttendShape& sh;
   SeqFn seq;
   int B, heads;
   int b, h, u;
@@ -108,10 +150,9 @@ struct AttendCursor {
   long long left;  // cost left in the run
   AttendSeq s;
 
-  SPECV_HD AttendCursor(AttendShape shape, SeqFn fn, int nseq, int nheads, int b_, int h_, int u_,
-                        int x_, long long left_)
-      : sh(shape), seq(fn), B(nseq), heads(nheads), b(b_), h(h_), u(u_), x(x_), left(left_) {
-    if (left > 0) s = seq(b);
+  SPECV_HD AttendCursor(const AttendShape& shape, SeqFn fn, int nseq, int nheads, int b_, int h_,
+                        int u_, int x_, long long left_, const AttendSeq& s_)
+      : sh(shape), seq(fn), B(nseq), heads(nheads), b(b_), h(h_), u(u_), x(x_), left(left_), s(s_) {
   }
   SPECV_HD bool next(AttendPiece* p) {
     while (left > 0) {
@@ -127,9 +168,9 @@ struct AttendCursor {
       p->nt = nt;
       p->t0 = x0 < nt ? x0 : nt;
       p->t1 = x < nt ? x : nt;
-      p->tok0 = u * 2 * sh.tpt;
+      p->tok0 = u * sh.w;
       const int rest = s.n - p->tok0;
-      p->ntok = rest < 2 * sh.tpt ? rest : 2 * sh.tpt;
+      p->ntok = rest < sh.w ? rest : sh.w;
       if (x == cost) {
         x = 0;
         if (++u == sh.units(s)) {

@@ -160,6 +160,9 @@ int attend_args(const void* q, int64_t ld_q, int dtype, const int32_t* row_off, 
   a->q_heads = q_heads;
   a->kv_heads = kv_heads;
   a->group = q_heads / kv_heads;
+  a->shape = attend_shape(a->group);
+  a->by_group = fast_div((uint32_t)a->group);
+  a->by_bs = fast_div(1);
   a->dim = head_dim;
   a->dtype = dtype;
   a->row_off = row_off;
@@ -1009,6 +1012,7 @@ int spec_attend_paged(const void* q, int64_t ld_q, int dtype, const int32_t* row
   a.max_blocks = max_blocks;
   a.num_blocks = num_blocks;
   a.block_size = block_size;
+  a.by_bs = fast_div((uint32_t)block_size);
   if (kv_stage) {
     a.stage_k = (const unsigned char*)kv_stage + layer * 2 * row;
     a.stage_v = a.stage_k + row;

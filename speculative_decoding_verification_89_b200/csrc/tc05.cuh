@@ -21,9 +21,12 @@ constexpr uint32_t mma_idesc(bool bf16, int M, int N, bool b_mn_major) {
 // stride offset steps over 8 rows of M or N (the leading one is unused).
 // MN-major: a row is 64 elements of N at one k; the stride offset steps
 // over 8 k, the leading offset over 64 elements of N.
-__device__ __forceinline__ uint64_t mma_sdesc(uint32_t addr, uint32_t lead_bytes) {
-  return (uint64_t)((addr >> 4) & 0x3fffu) | ((uint64_t)((lead_bytes >> 4) & 0x3fffu) << 16) |
-         ((uint64_t)(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// The low word is (address | leading offset << 16) / 16, the high one the same for all.
+__device__ __forceinline__ uint64_t mma_sdesc(uint32_t low) {
+  constexpr uint32_t kHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(low), "r"(kHigh));
+  return r;
 }
 
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t cols) {
