@@ -45,7 +45,7 @@ struct Tile {
 };
 
 struct Shared {
-  uint64_t full[13], empty[13];
+  uint64_t full[13], empty[13], landed[13];
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t o_empty, swap, drain;
   uint32_t tmem;
@@ -291,24 +291,32 @@ __device__ __forceinline__ bool piece_program(const AttendShape& shape, const At
 // ---------------------------------------------------------------------------
 // Loading: query rows, then K and V tiles in the order they are used
 // ---------------------------------------------------------------------------
+// Warp 9 copies columns 0-63 and warp 10 columns 64-127 of each tile with tiled
+// (TMA) copies: one for a query tile or 128 packed rows, one per page for the
+// pool. Warp 11 puts right what the copies of a sequence's last tiles cannot:
+// V rows past the keys are set to zero (what lies there must not reach a
+// product: a weight of 0 times a NaN) and staged rows are put in their place.
+// A tile is full when all three warps have arrived. Pages that no box fits
+// are copied row by row by all three.
 template <int DP>
 struct Loader {
-  static constexpr int kChunks = DP / 8;                // 16-byte chunks of a row
-  static constexpr int kRowStep = kLoaders / kChunks;   // rows between a thread's rows
+  static constexpr int kChunks = DP / 8;   // 16-byte chunks of a row
   const AttendArgs& a;
   Shared* sh;
-  uint32_t tiles;   // shared address of the tiles
-  int lt;           // 0 .. 95
+  uint32_t tiles;     // shared address of the tiles
+  int role, lane;     // 0-2: columns 0-63, columns 64-127, mending
   Buffers<Tile<DP>::kCount> buf;
   AttendPiece p;
+  int pooled;         // keys of the sequence in the pool (or packed rows)
   int q_buf[2], k_buf, v_buf;
-  uint32_t issued;  // buffers filled at least once, by bit
+  uint32_t issued;    // buffers filled at least once, by bit
+  uint32_t land_ph;   // parity of each buffer's next use of `landed`
   // Table entries of 32 consecutive pages, one per lane: the group that the K
   // tiles have reached, the one before (V tiles follow) and the next one.
   int group, cur, prev, next;
 
-  __device__ Loader(const AttendArgs& a_, Shared* s, uint32_t t, int l)
-      : a(a_), sh(s), tiles(t), lt(l), issued(0) {}
+  __device__ Loader(const AttendArgs& a_, Shared* s, uint32_t t, int thread)
+      : a(a_), sh(s), tiles(t), role(thread >> 5), lane(thread & 31), issued(0), land_ph(0) {}
   __device__ bool wait(uint64_t* bar, uint32_t ph) {
     return __all_sync(0xffffffffu, wait_bar(bar, ph, sh, a.status));
   }
@@ -329,70 +337,81 @@ struct Loader {
     return true;
   }
   __device__ uint32_t tile(int b) const { return tiles + b * Tile<DP>::kBytes; }
-  __device__ uint32_t chunk_addr(uint32_t tile, int row) const {
-    const int c = lt % kChunks;
-    return tile + (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
-  }
   __device__ int entry(int page) const {
     return page < a.max_blocks ? a.tables[(long long)p.b * a.max_blocks + page] : 0;
   }
-  __device__ int first_page(int t) const { return (int)a.by_bs((uint32_t)(t * kTileKeys)); }
+  __device__ int page_of(int key) const { return (int)a.by_bs((uint32_t)key); }
+  __device__ bool copies() const { return role == 0 || (role == 1 && a.dim > 64); }
   __device__ void begin() {
+    pooled = a.stage_k ? p.s.len - p.s.n : p.s.len;
     if (!a.tables || !a.box_rows || p.t1 == p.t0) return;
-    group = first_page(p.t0) >> 5;
-    cur = entry(group * 32 + (lt & 31));
-    next = entry(group * 32 + 32 + (lt & 31));
+    group = page_of(p.t0 * kTileKeys) >> 5;
+    cur = entry(group * 32 + lane);
+    next = entry(group * 32 + 32 + lane);
     prev = 0;
   }
+  // This warp's columns of query tile w: rows (token, head of the group).
   __device__ bool take_q(int w) {
     if (!take(&q_buf[w])) return false;
-    const uint32_t dst = tile(q_buf[w]);
-    const int c = lt % kChunks, tpt = a.shape.tpt;
-    const int tok0 = p.tok0 + w * tpt, rows = min(p.ntok - w * tpt, tpt) * a.group;
-    const unsigned char* base =
-        a.q + (long long)(p.s.row0 + tok0) * a.ld_q + ((long long)p.h * a.group * a.dim + c * 8) * 2;
-#pragma unroll 4
-    for (int r = lt / kChunks; r < 128; r += kRowStep) {
-      const int t = (int)a.by_group((uint32_t)r), g = r - t * a.group;
-      const bool ok = r < rows && c * 8 < a.dim;
-      const unsigned char* src = ok ? base + t * a.ld_q + g * a.dim * 2 : a.q;
-      cp_async16(chunk_addr(dst, r), src, ok ? 16u : 0u);
+    uint64_t* bar = &sh->full[q_buf[w]];
+    const int tok0 = p.s.row0 + p.tok0 + w * a.shape.tpt;
+    const uint32_t bytes = a.shape.tpt * a.group * 128;
+    const uint32_t dst = tile(q_buf[w]) + role * (128 * 128);
+    if (elect_one()) {
+      if (copies()) {
+        mbar_arrive_expect_tx(bar, bytes);
+        tma_box4(dst, &a.map_q, role * 64, 0, p.h, tok0, bar);
+      } else {
+        mbar_arrive(bar);
+      }
     }
-    cp_async_arrive(&sh->full[q_buf[w]]);
     return true;
   }
   __device__ bool take_k(int i) { return take(&k_buf) && load_kv(p.t0 + i, 0, k_buf); }
   __device__ bool take_v(int i) { return take(&v_buf) && load_kv(p.t0 + i, 1, v_buf); }
-  // K (v = 0) or V (v = 1) rows of tile t of the piece's sequence. A tile whose
-  // 128 keys all lie in the packed rows or the pool comes by tiled copies, one
-  // per page and 64 columns; others (a sequence's last, staged rows, pages that
-  // no box fits) row by row, with zeros for rows past the keys, so what lies
-  // there cannot reach a product.
+  // K (v = 0) or V (v = 1) rows of tile t of the piece's sequence.
   __device__ bool load_kv(int t, int v, int b) {
-    const int pooled = a.stage_k ? p.s.len - p.s.n : p.s.len;
-    if (a.box_rows && (t + 1) * kTileKeys <= pooled) {
-      load_boxes(t, v, tile(b), &sh->full[b]);
-    } else {
-      load_rows(t, v, tile(b), pooled);
-      cp_async_arrive(&sh->full[b]);
+    if (!a.box_rows) {
+      load_rows(t, v, tile(b));
+      if (elect_one()) mbar_arrive(&sh->full[b]);
+      return true;
     }
+    const bool mend = (t + 1) * kTileKeys > pooled && (v || a.stage_k);
+    uint64_t* bar = mend ? &sh->landed[b] : &sh->full[b];
+    if (role == 2 && mend) {
+      if (!mend_tile(t, v, b)) return false;
+    } else if (copies()) {
+      if (elect_one()) {
+        mbar_arrive_expect_tx(bar, 128 * 128);
+        if (mend) mbar_arrive(&sh->full[b]);
+      }
+      load_boxes(t, v, tile(b) + role * (128 * 128), bar);
+    } else if (elect_one()) {
+      if (mend) mbar_arrive(&sh->landed[b]);
+      mbar_arrive(&sh->full[b]);
+    }
+    if (mend) land_ph ^= 1u << b;
     return true;
   }
-  // 64 columns per warp; one lane announces the bytes and issues the copies.
+  template <int kBoxes>
+  __device__ void page_boxes(const void* map, uint32_t dst, int first, int row, int id,
+                             uint64_t* bar) {
+    int from[kBoxes];
+#pragma unroll
+    for (int i = 0; i < kBoxes; ++i) from[i] = __shfl_sync(0xffffffffu, id, first + i);
+    if (elect_one()) {
+#pragma unroll
+      for (int i = 0; i < kBoxes; ++i)
+        tma_box4(dst + i * (kTileKeys / kBoxes) * 128, map, role * 64, p.h, row, from[i], bar);
+    }
+  }
   __device__ void load_boxes(int t, int v, uint32_t dst, uint64_t* bar) {
-    const int half = lt >> 5, lane = lt & 31;
-    const bool mine = half * 64 < a.dim && half < 2;
-    const bool one = elect_one();
-    if (!mine || !one) mbar_arrive(bar);
-    if (!mine) return;
     const void* map = v ? &a.map_v : &a.map_k;
-    dst += half * (128 * 128);
-    if (one) mbar_arrive_expect_tx(bar, 128 * 128);
     if (!a.tables) {
-      if (one) tma_box3(dst, map, half * 64, p.h, p.s.row0 + t * kTileKeys, bar);
+      if (elect_one()) tma_box3(dst, map, role * 64, p.h, p.s.row0 + t * kTileKeys, bar);
       return;
     }
-    const int page = first_page(t), g = page >> 5;
+    const int page = page_of(t * kTileKeys), g = page >> 5;
     if (!v && g != group) {
       prev = cur;
       cur = next;
@@ -400,36 +419,84 @@ struct Loader {
       next = entry(g * 32 + 32 + lane);
     }
     int id = g == group ? cur : prev;
-    const int row = t * kTileKeys - page * a.block_size;  // of the first page, if it is larger than a tile
+    const int row = t * kTileKeys - page * a.block_size;  // not 0 in a page larger than a tile
     const int boxes = kTileKeys / a.box_rows;
-    const bool used = (unsigned)(lane - (page & 31)) < (unsigned)boxes;
-    if (id < 0 || id >= a.num_blocks) {
-      if (used) set_status(a.status, SPEC_EDEVICE);
+    const bool held = (g * 32 + lane) * (long long)a.block_size < pooled;
+    if (!held || id < 0 || id >= a.num_blocks) {
+      if (held && (unsigned)(lane - (page & 31)) < (unsigned)boxes)
+        set_status(a.status, SPEC_EDEVICE);
       id = a.num_blocks;  // outside the tensor: zeros
     }
-#pragma unroll 4
-    for (int i = 0; i < boxes; ++i) {
-      const int from = __shfl_sync(0xffffffffu, id, (page & 31) + i);
-      if (one)
-        tma_box4(dst + i * a.box_rows * 128, map, half * 64, p.h, row, from, bar);
-    }
+    if (boxes == 8) page_boxes<8>(map, dst, page & 31, row, id, bar);
+    else if (boxes == 1) page_boxes<1>(map, dst, page & 31, row, id, bar);
+    else if (boxes == 2) page_boxes<2>(map, dst, page & 31, row, id, bar);
+    else if (boxes == 4) page_boxes<4>(map, dst, page & 31, row, id, bar);
+    else page_boxes<16>(map, dst, page & 31, row, id, bar);
   }
-  __device__ void load_rows(int t, int v, uint32_t dst, int pooled) {
-    const int c = lt % kChunks;
+  __device__ uint32_t chunk_addr(uint32_t tile, int row, int c) const {
+    return tile + (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+  }
+  // Warp 11, once the copies have landed: staged rows to their places, zeros
+  // in the V rows past the keys that the copies may have filled.
+  __device__ bool mend_tile(int t, int v, int b) {
+    constexpr int kRows = 32 / kChunks;  // rows of a step
+    constexpr int kAhead = 8;
+    const int c = lane % kChunks, key0 = t * kTileKeys;
+    const int first = max(0, pooled - key0);             // first row not from the pool
+    const int end = min(kTileKeys, p.s.len - key0);      // first row past the keys
+    const int staged = a.stage_k ? max(0, end - first) : 0;
+    const unsigned char* src = nullptr;
+    if (staged)
+      src = (v ? a.stage_v : a.stage_k) + p.b * a.stage_seq +
+            (long long)(key0 + first - pooled) * a.stage_row + ((long long)p.h * a.dim + c * 8) * 2;
+    const uint32_t dst = tile(b);
+    uint4 x[kAhead];
+    const int r0 = lane / kChunks;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int r = r0 + i * kRows;
+      x[i] = r < staged && c * 8 < a.dim
+                 ? __ldg(reinterpret_cast<const uint4*>(src + r * a.stage_row))
+                 : make_uint4(0, 0, 0, 0);
+    }
+    if (!wait(&sh->landed[b], (land_ph >> b) & 1)) return false;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int r = r0 + i * kRows;
+      if (r < staged) st_shared16(chunk_addr(dst, first + r, c), x[i]);
+    }
+    for (int r = r0 + kAhead * kRows; r < staged; r += kRows)
+      st_shared16(chunk_addr(dst, first + r, c),
+                  c * 8 < a.dim ? __ldg(reinterpret_cast<const uint4*>(src + r * a.stage_row))
+                                : make_uint4(0, 0, 0, 0));
+    if (v) {
+      int stop = kTileKeys;  // pages past the last are zeros already
+      if (a.tables) {
+        const int last = pooled > 0 ? page_of(pooled - 1) + 1 : 0;
+        stop = (int)min((long long)kTileKeys, (long long)last * a.block_size - key0);
+      }
+      for (int r = first + staged + r0; r < stop; r += kRows)
+        st_shared16(chunk_addr(dst, r, c), make_uint4(0, 0, 0, 0));
+    }
+    fence_proxy_async_smem();
+    if (elect_one_after_sync()) mbar_arrive(&sh->full[b]);
+    return true;
+  }
+  __device__ void load_rows(int t, int v, uint32_t dst) {
+    constexpr int kStep = kLoaders / kChunks;
+    const int thread = role * 32 + lane, c = thread % kChunks;
     const long long col = ((long long)p.h * a.dim + c * 8) * 2;
     const unsigned char* base = v ? a.v : a.k;
     const long long ld = v ? a.ld_v : a.ld_k;
-    const int32_t* table = a.tables ? a.tables + (long long)p.b * a.max_blocks : nullptr;
+    const int32_t* table = a.tables + (long long)p.b * a.max_blocks;
     bool bad = false;
 #pragma unroll 8
-    for (int r = lt / kChunks; r < 128; r += kRowStep) {
+    for (int r = thread / kChunks; r < kTileKeys; r += kStep) {
       const int key = t * kTileKeys + r;
       bool ok = key < p.s.len && c * 8 < a.dim;
       const unsigned char* src = base;
-      if (!table) {
-        src = base + (p.s.row0 + (ok ? key : 0)) * ld + col;
-      } else if (key < pooled) {
-        const int blk = (int)a.by_bs((uint32_t)key);
+      if (key < pooled) {
+        const int blk = page_of(key);
         int id = ok ? table[blk] : 0;
         if (id < 0 || id >= a.num_blocks) {
           bad = true;
@@ -440,9 +507,16 @@ struct Loader {
       } else if (ok) {
         src = (v ? a.stage_v : a.stage_k) + p.b * a.stage_seq + (key - pooled) * a.stage_row + col;
       }
-      cp_async16(chunk_addr(dst, r), src, ok ? 16u : 0u);
+      cp_async16(chunk_addr(dst, r, c), src, ok ? 16u : 0u);
     }
     if (bad) set_status(a.status, SPEC_EDEVICE);
+    cp_async_wait_all();
+    fence_proxy_async_smem();
+    __syncwarp();
+  }
+  __device__ bool elect_one_after_sync() {
+    __syncwarp();
+    return elect_one();
   }
   __device__ void give_q(int w) { buf.give(q_buf[w]); }
   __device__ void give_k() { buf.give(k_buf); }
@@ -612,8 +686,8 @@ struct Softmax {
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
   }
   // Scores of one tile to p~; m is the reference and l the sum, both of this row.
-  __device__ bool tile(int key0, int limit, int warp_limit, bool live, bool first, float& m,
-                       float& l) {
+  __device__ bool tile(int key0, int limit, int warp_limit, bool live, bool valid, bool first,
+                       float& m, float& l) {
     if (!wait(&sh->s_full[w], s_ph)) return false;
     s_ph ^= 1;
     if (live) {
@@ -641,7 +715,7 @@ struct Softmax {
       for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], __uint_as_float(s[124 + j]));
       const float top =
           fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
-      const bool raise = top > m + kSlack || (m == -INFINITY && top > m);
+      const bool raise = valid && (top > m + kSlack || (m == -INFINITY && top > m));
       if (__any_sync(0xffffffffu, raise)) {
         const float f = weight(m, fmaxf(m, top));
         m = fmaxf(m, top);
@@ -704,13 +778,27 @@ struct Softmax {
       for (int i = 0; i < 32; ++i) o[i] = f1 == 0.0f ? o[i] : fmaf(f1, __uint_as_float(x[i]), o[i]);
     }
   }
+  // A thread's 32 columns; 32-byte sectors where the rows begin on them.
   __device__ void write_out(unsigned char* dst, int c0, const float (&o)[32]) {
+    uint32_t x[16];
 #pragma unroll
-    for (int i = 0; i < 32; i += 8)
-      if (c0 + i < a.dim)
-        *reinterpret_cast<uint4*>(dst + (c0 + i) * 2) =
-            make_uint4(Pack<T>::two(o[i], o[i + 1]), Pack<T>::two(o[i + 2], o[i + 3]),
-                       Pack<T>::two(o[i + 4], o[i + 5]), Pack<T>::two(o[i + 6], o[i + 7]));
+    for (int i = 0; i < 16; ++i) x[i] = Pack<T>::two(o[2 * i], o[2 * i + 1]);
+#pragma unroll
+    for (int i = 0; i < 16; i += 8) {
+      unsigned char* d = dst + (c0 + 2 * i) * 2;
+      if (a.out_sectors) {
+        if (c0 + 2 * i < a.dim)
+          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d),
+                       "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3]), "r"(x[i + 4]),
+                       "r"(x[i + 5]), "r"(x[i + 6]), "r"(x[i + 7])
+                       : "memory");
+      } else {
+        if (c0 + 2 * i < a.dim)
+          *reinterpret_cast<uint4*>(d) = make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+        if (c0 + 2 * i + 8 < a.dim)
+          *reinterpret_cast<uint4*>(d + 16) = make_uint4(x[i + 4], x[i + 5], x[i + 6], x[i + 7]);
+      }
+    }
   }
   __device__ void run() {
     const AttendShape& shape = a.shape;
@@ -732,7 +820,7 @@ struct Softmax {
       float m = -INFINITY, l = 0.0f;
       for (int i = 0; i < mine; ++i) {
         const int t = p.t0 + (two ? i : 2 * i + w);
-        if (!tile(t * kTileKeys, limit, warp_limit, live, i == 0, m, l)) return;
+        if (!tile(t * kTileKeys, limit, warp_limit, live, valid, i == 0, m, l)) return;
       }
       if (p.t0 > 0) {
         rec.first = 1;
@@ -824,8 +912,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   const int tid = threadIdx.x, warp = tid >> 5;
   if (tid == 0) {
     for (int i = 0; i < Tile<DP>::kCount; ++i) {
-      mbar_init(&sh->full[i], kLoaders);
+      mbar_init(&sh->full[i], 3);
       mbar_init(&sh->empty[i], 1);
+      mbar_init(&sh->landed[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh->s_full[i], 1);
@@ -861,7 +950,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     Loader<DP> s(a, sh, tiles, tid - 9 * 32);
     s.run();
-    cp_async_wait_all();
     if (*(volatile int*)&sh->abort) s.drain();
   }
   __syncwarp();
@@ -962,38 +1050,49 @@ EncodeFn encode_fn() {
 }
 }  // namespace
 
-// Packed rows: (column, head, row), boxes of 128 rows. Pages: (column, head,
-// row, block), boxes of a whole page where its rows divide the tile, or of 128
-// rows where the tile's rows divide the page; a box begins on a whole 1024-byte
-// swizzle atom, so pages of fewer than 8 rows are left to the row copies.
-// Columns past the head's end are filled with zeros.
-void attend_maps(AttendArgs* a) {
-  a->box_rows = 0;
-  const int bs = a->block_size;
-  int rows = kTileKeys;
-  if (a->tables) {
-    if (bs % kTileKeys != 0) rows = (bs >= 8 && kTileKeys % bs == 0) ? bs : 0;
+// Query rows: (column, head of the group, K/V head, row), a box holds the
+// whole tokens of a tile in the order of the tile's rows. Packed K/V rows: (column,
+// head, row), boxes of 128 rows. Pages: (column, head, row, block), boxes of a
+// whole page where its rows divide the tile, or of 128 rows where the tile's
+// rows divide the page; a box begins on a whole 1024-byte swizzle atom, so
+// pages of fewer than 8 rows are left to the row copies. Boxes have 64 columns;
+// those past the head's end are filled with zeros.
+cudaError_t attend_maps(AttendArgs* a) {
+  const EncodeFn encode = encode_fn();
+  if (!encode) return cudaErrorNotSupported;
+  auto form = [&](CUtensorMap* map, const void* p, cuuint32_t rank, const cuuint64_t* dims,
+                  const cuuint64_t* strides, const cuuint32_t* box) {
+    const cuuint32_t step[4] = {1, 1, 1, 1};
+    return encode(map,
+                  a->dtype == SPEC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                  rank, const_cast<void*>(p), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  const cuuint64_t head = (cuuint64_t)a->dim * 2;
+  {
+    const cuuint64_t dims[4] = {(cuuint64_t)a->dim, (cuuint64_t)a->group, (cuuint64_t)a->kv_heads,
+                                (cuuint64_t)a->T};
+    const cuuint64_t strides[3] = {head, head * a->group, (cuuint64_t)a->ld_q};
+    const cuuint32_t box[4] = {64, (cuuint32_t)a->group, 1, (cuuint32_t)a->shape.tpt};
+    if (!form(&a->map_q, a->q, 4, dims, strides, box)) return cudaErrorInvalidValue;
   }
-  const EncodeFn encode = rows ? encode_fn() : nullptr;
-  if (!encode) return;
-  const cuuint32_t rank = a->tables ? 4 : 3;
+  const int bs = a->block_size;
+  a->box_rows = kTileKeys;
+  if (a->tables && bs % kTileKeys != 0) a->box_rows = (bs >= 8 && kTileKeys % bs == 0) ? bs : 0;
+  if (!a->box_rows) return cudaSuccess;
   for (int v = 0; v < 2; ++v) {
-    const cuuint64_t ld = (cuuint64_t)(v ? a->ld_v : a->ld_k);
     const cuuint64_t dims[4] = {(cuuint64_t)a->dim, (cuuint64_t)a->kv_heads,
                                 (cuuint64_t)(a->tables ? bs : a->T), (cuuint64_t)a->num_blocks};
-    const cuuint64_t strides[3] = {(cuuint64_t)a->dim * 2, ld, (cuuint64_t)a->page_bytes};
-    const cuuint32_t box[4] = {64, 1, (cuuint32_t)rows, 1};
-    const cuuint32_t step[4] = {1, 1, 1, 1};
-    if (encode(v ? &a->map_v : &a->map_k,
-               a->dtype == SPEC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                     : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-               rank, const_cast<unsigned char*>(v ? a->v : a->k), dims, strides, box, step,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return;
+    const cuuint64_t strides[3] = {head, (cuuint64_t)(v ? a->ld_v : a->ld_k),
+                                   (cuuint64_t)a->page_bytes};
+    const cuuint32_t box[4] = {64, 1, (cuuint32_t)a->box_rows, 1};
+    if (!form(v ? &a->map_v : &a->map_k, v ? a->v : a->k, a->tables ? 4 : 3, dims, strides, box))
+      return cudaErrorInvalidValue;
   }
-  a->box_rows = rows;
+  return cudaSuccess;
 }
 
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {

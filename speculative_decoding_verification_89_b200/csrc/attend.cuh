@@ -51,13 +51,14 @@ struct AttendArgs {
   float2* part_ml;   // [2 * ctas][2 * kTileRows] (maximum in log2 units, sum)
   AttendRec* rec;    // [ctas]
   int ctas;
-  // K and V as tensors (column, head, row, block) for tiled copies of box_rows
-  // rows of 64 columns each; box_rows 0: none, rows are copied one by one.
+  bool out_sectors;   // rows of heads in out begin on 32-byte boundaries
+  // Tensors for tiled copies of 64 columns; those of K and V have box_rows rows,
+  // 0: the pages fit no box and rows are copied one by one.
   int box_rows;
-  CUtensorMap map_k, map_v;
+  CUtensorMap map_q, map_k, map_v;
 };
-// Forms the maps where the layout allows tiled copies (attend.cu says which).
-void attend_maps(AttendArgs* a);
+// Forms the maps.
+cudaError_t attend_maps(AttendArgs* a);
 // Workspace bytes of the parts, for rows padded to DP columns.
 struct AttendWs {
   size_t o, ml, rec, total;

@@ -171,6 +171,7 @@ int attend_args(const void* q, int64_t ld_q, int dtype, const int32_t* row_off, 
   a->ld_q = ld_q * 2;
   a->out = (unsigned char*)out;
   a->ld_out = ld_out * 2;
+  a->out_sectors = aligned(out, 32) && (ld_out * 2) % 32 == 0 && (head_dim * 2) % 32 == 0;
   a->lse = lse;
   a->status = dev_status;
   a->part_o = reinterpret_cast<float*>((char*)ws + w.o);
@@ -978,8 +979,9 @@ int spec_attend_prompt(const void* q, int64_t ld_q, const void* k, int64_t ld_k,
   a.v = (const unsigned char*)v;
   a.ld_k = ld_k * 2;
   a.ld_v = ld_v * 2;
-  attend_maps(&a);
-  return cuda_status(launch_attend(a, (cudaStream_t)stream));
+  cudaError_t e = attend_maps(&a);
+  if (e == cudaSuccess) e = launch_attend(a, (cudaStream_t)stream);
+  return cuda_status(e);
 }
 
 int spec_attend_paged(const void* q, int64_t ld_q, int dtype, const int32_t* row_off,
@@ -1020,8 +1022,9 @@ int spec_attend_paged(const void* q, int64_t ld_q, int dtype, const int32_t* row
     a.stage_seq = Kp1 * a.stage_row;
     a.stage_rows = Kp1;
   }
-  attend_maps(&a);
-  return cuda_status(launch_attend(a, (cudaStream_t)stream));
+  cudaError_t e = attend_maps(&a);
+  if (e == cudaSuccess) e = launch_attend(a, (cudaStream_t)stream);
+  return cuda_status(e);
 }
 
 const char* spec_last_cuda_error(void) { return cudaGetErrorString(g_last_cuda); }
