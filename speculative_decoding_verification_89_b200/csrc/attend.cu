@@ -122,6 +122,12 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
   return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
+// The cost of a sequence under one head; of one unit without the general sum.
+__device__ __forceinline__ long long cost_of_head(const AttendShape& shape, const AttendSeq& s) {
+  if (s.n <= 0) return 0;
+  return s.n <= shape.w ? shape.tiles_upto(s, s.n - 1) + kUnitCost : shape.head_cost(s);
+}
+
 // Where this CTA's run of the cost line starts, into sh; all threads.
 __device__ __forceinline__ void find_run(const AttendArgs& a, Shared* sh) {
   const SeqOf seq{&a};
@@ -133,7 +139,7 @@ __device__ __forceinline__ void find_run(const AttendArgs& a, Shared* sh) {
   int bad = 0;
   for (int b = b0; b < b1; ++b) {
     const AttendSeq s = seq.get(b, &bad);
-    sum += shape.head_cost(s) * a.kv_heads;
+    sum += cost_of_head(shape, s) * a.kv_heads;
   }
   if (bad && blockIdx.x == 0) set_status(a.status, SPEC_EDEVICE);
   long long incl = sum;
@@ -157,7 +163,7 @@ __device__ __forceinline__ void find_run(const AttendArgs& a, Shared* sh) {
   if (from < to && from >= at && from < at + sum) {
     for (int b = b0; b < b1; ++b) {
       const AttendSeq s = seq(b);
-      const long long head = shape.head_cost(s);
+      const long long head = cost_of_head(shape, s);
       if (from < at + head * a.kv_heads) {
         const int h = (int)quotient(from - at, head);
         const long long y = from - at - h * head;
@@ -170,7 +176,7 @@ __device__ __forceinline__ void find_run(const AttendArgs& a, Shared* sh) {
         sh->start[0] = b;
         sh->start[1] = h;
         sh->start[2] = lo;
-        sh->start[3] = (int)(y - shape.cost_before(s, lo));
+        sh->start[3] = (int)(lo ? y - shape.cost_before(s, lo) : y);
         sh->run = to - from;
         break;
       }
@@ -227,61 +233,46 @@ __device__ __forceinline__ int first_tile_count(const AttendShape& shape, const 
   return max(0, min(p.t1, nt0) - p.t0);
 }
 
-// The program of a piece that the loading warps (which fill what is taken)
-// and the issuing warp (which uses it) share. Side:
-//   take_q(w), take_k(t), take_v(t): the next buffer, for the query tile of
-//     warpgroup w, K or V tile t; a K tile lasts until give_k, V until give_v;
-//   qk(w), pv(w, first, last): the products; give_q(w).
+// The program of a piece. Two query tiles: both use each K
+// and V tile, the first may need fewer of them; K tiles are one ahead of the V
+// tiles. One query tile: the K/V tiles go to the two accumulators in turn, K
+// two ahead. Side:
+//   take_q(w), take_k(t), take_v(t): the next buffer, for query tile w, K or V
+//     tile t; give_q(w), give_k(), give_v(): it is free once what was issued is done;
+//   qk(w, x): scores of accumulator w with query tile x; begin_pv(): before the
+//     first pv; pv(w, first, last): weights times V.
+// Every step is written once: the code of both sides has to stay small enough
+// for the instruction cache beside the softmax warps' (unrolled by case it was
+// 376 KB, and the prompt of 8192 rows took 514 us).
+// (The loading warps' side is Loader::fill: the same takes and gives in the
+// same order, with one place that loads.)
 template <typename Side>
 __device__ __forceinline__ bool piece_program(const AttendShape& shape, const AttendPiece& p,
                                               Side& side) {
   const int m = p.t1 - p.t0;
   if (m == 0) return true;  // rows that see nothing
-  if (p.ntok > shape.tpt) {
-    // Two query tiles share each K/V tile; the first may need fewer of them.
-    const int c0 = first_tile_count(shape, p);
-    if (!side.take_q(0) || !side.take_q(1) || !side.take_k(0)) return false;
-    if (c0 > 0) side.qk(0);
-    if (c0 <= 1) side.give_q(0);
-    side.qk(1);
-    side.give_k();
-    if (m == 1) side.give_q(1);
-    if (!side.begin_pv()) return false;
-    for (int i = 0; i < m; ++i) {
-      const bool more = i + 1 < m;
-      if (!side.take_v(i)) return false;
-      if (i < c0 && !side.pv(0, i == 0, i == c0 - 1)) return false;
+  const bool two = p.ntok > shape.tpt;
+  const int ahead = two ? 1 : 2, c0 = two ? first_tile_count(shape, p) : m;
+#pragma unroll 1
+  for (int w = 0; w < (two ? 2 : 1); ++w)
+    if (!side.take_q(w)) return false;
+#pragma unroll 1
+  for (int i = -ahead; i < m; ++i) {
+    const bool more = i + ahead < m;
+    if (i == 0 && !side.begin_pv()) return false;
+    if (i >= 0 && !side.take_v(i)) return false;
+    const int w0 = two ? 0 : i & 1, w1 = two ? 1 : w0;
+#pragma unroll 1
+    for (int w = w0; w <= w1; ++w) {
+      const int x = two ? w : 0;           // its query tile
+      const int count = x ? m : c0;        // K/V tiles that this one needs
+      if (i >= 0 && i < count && !side.pv(w, i < ahead, i + ahead >= count)) return false;
+      if (i >= 0 && w == w1) side.give_v();
       if (more) {
-        if (!side.take_k(i + 1)) return false;
-        if (i + 1 < c0) side.qk(0);
-        if (i + 1 == c0 - 1) side.give_q(0);
-      }
-      if (!side.pv(1, i == 0, !more)) return false;
-      side.give_v();
-      if (more) {
-        side.qk(1);
-        side.give_k();
-        if (i + 2 == m) side.give_q(1);
-      }
-    }
-  } else {
-    // One query tile; the K/V tiles go to the two accumulators in turn.
-    if (!side.take_q(0)) return false;
-    for (int i = 0; i < min(2, m); ++i) {
-      if (!side.take_k(i)) return false;
-      side.qk(i);
-      side.give_k();
-    }
-    if (m <= 2) side.give_q(0);
-    if (!side.begin_pv()) return false;
-    for (int i = 0; i < m; ++i) {
-      if (!side.take_v(i) || !side.pv(i & 1, i < 2, i + 2 >= m)) return false;
-      side.give_v();
-      if (i + 2 < m) {
-        if (!side.take_k(i + 2)) return false;
-        side.qk(i & 1);
-        side.give_k();
-        if (i + 3 == m) side.give_q(0);
+        if (w == w0 && !side.take_k(i + ahead)) return false;
+        if (i + ahead < count) side.qk(w, x);
+        if (i + ahead == max(count - 1, 0)) side.give_q(x);
+        if (w == w1) side.give_k();
       }
     }
   }
@@ -308,7 +299,7 @@ struct Loader {
   Buffers<Tile<DP>::kCount> buf;
   AttendPiece p;
   int pooled;         // keys of the sequence in the pool (or packed rows)
-  int q_buf[2], k_buf, v_buf;
+  int q_buf[2];
   uint32_t issued;    // buffers filled at least once, by bit
   uint32_t land_ph;   // parity of each buffer's next use of `landed`
   // Table entries of 32 consecutive pages, one per lane: the group that the K
@@ -352,11 +343,13 @@ struct Loader {
   }
   // This warp's columns of query tile w: rows (token, head of the group).
   __device__ bool take_q(int w) {
-    if (!take(&q_buf[w])) return false;
-    uint64_t* bar = &sh->full[q_buf[w]];
+    int b;
+    if (!take(&b)) return false;
+    if (w) q_buf[1] = b; else q_buf[0] = b;
+    uint64_t* bar = &sh->full[b];
     const int tok0 = p.s.row0 + p.tok0 + w * a.shape.tpt;
     const uint32_t bytes = a.shape.tpt * a.group * 128;
-    const uint32_t dst = tile(q_buf[w]) + role * (128 * 128);
+    const uint32_t dst = tile(b) + role * (128 * 128);
     if (elect_one()) {
       if (copies()) {
         mbar_arrive_expect_tx(bar, bytes);
@@ -367,8 +360,6 @@ struct Loader {
     }
     return true;
   }
-  __device__ bool take_k(int i) { return take(&k_buf) && load_kv(p.t0 + i, 0, k_buf); }
-  __device__ bool take_v(int i) { return take(&v_buf) && load_kv(p.t0 + i, 1, v_buf); }
   // K (v = 0) or V (v = 1) rows of tile t of the piece's sequence.
   __device__ bool load_kv(int t, int v, int b) {
     if (!a.box_rows) {
@@ -427,11 +418,13 @@ struct Loader {
         set_status(a.status, SPEC_EDEVICE);
       id = a.num_blocks;  // outside the tensor: zeros
     }
-    if (boxes == 8) page_boxes<8>(map, dst, page & 31, row, id, bar);
-    else if (boxes == 1) page_boxes<1>(map, dst, page & 31, row, id, bar);
-    else if (boxes == 2) page_boxes<2>(map, dst, page & 31, row, id, bar);
-    else if (boxes == 4) page_boxes<4>(map, dst, page & 31, row, id, bar);
-    else page_boxes<16>(map, dst, page & 31, row, id, bar);
+    if (boxes == 8) {  // pages of 16 rows: the numbers first, then all copies in a row
+      page_boxes<8>(map, dst, page & 31, row, id, bar);
+      return;
+    }
+#pragma unroll 1
+    for (int i = 0; i < boxes; ++i)
+      page_boxes<1>(map, dst + i * a.box_rows * 128, (page & 31) + i, row, id, bar);
   }
   __device__ uint32_t chunk_addr(uint32_t tile, int row, int c) const {
     return tile + (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
@@ -440,7 +433,7 @@ struct Loader {
   // in the V rows past the keys that the copies may have filled.
   __device__ bool mend_tile(int t, int v, int b) {
     constexpr int kRows = 32 / kChunks;  // rows of a step
-    constexpr int kAhead = 8;
+    constexpr int kAhead = 4;
     const int c = lane % kChunks, key0 = t * kTileKeys;
     const int first = max(0, pooled - key0);             // first row not from the pool
     const int end = min(kTileKeys, p.s.len - key0);      // first row past the keys
@@ -465,6 +458,7 @@ struct Loader {
       const int r = r0 + i * kRows;
       if (r < staged) st_shared16(chunk_addr(dst, first + r, c), x[i]);
     }
+#pragma unroll 1
     for (int r = r0 + kAhead * kRows; r < staged; r += kRows)
       st_shared16(chunk_addr(dst, first + r, c),
                   c * 8 < a.dim ? __ldg(reinterpret_cast<const uint4*>(src + r * a.stage_row))
@@ -475,6 +469,7 @@ struct Loader {
         const int last = pooled > 0 ? page_of(pooled - 1) + 1 : 0;
         stop = (int)min((long long)kTileKeys, (long long)last * a.block_size - key0);
       }
+#pragma unroll 1
       for (int r = first + staged + r0; r < stop; r += kRows)
         st_shared16(chunk_addr(dst, r, c), make_uint4(0, 0, 0, 0));
     }
@@ -490,7 +485,7 @@ struct Loader {
     const long long ld = v ? a.ld_v : a.ld_k;
     const int32_t* table = a.tables + (long long)p.b * a.max_blocks;
     bool bad = false;
-#pragma unroll 8
+#pragma unroll 2
     for (int r = thread / kChunks; r < kTileKeys; r += kStep) {
       const int key = t * kTileKeys + r;
       bool ok = key < p.s.len && c * 8 < a.dim;
@@ -518,17 +513,38 @@ struct Loader {
     __syncwarp();
     return elect_one();
   }
-  __device__ void give_q(int w) { buf.give(q_buf[w]); }
-  __device__ void give_k() { buf.give(k_buf); }
-  __device__ void give_v() { buf.give(v_buf); }
-  __device__ void qk(int) {}
-  __device__ bool pv(int, bool, bool) { return true; }
-  __device__ bool begin_pv() { return true; }
+  // The loads of a piece, in piece_program's order of takes and gives.
+  __device__ bool fill() {
+    const int m = p.t1 - p.t0;
+    if (m == 0) return true;
+    const bool two = p.ntok > a.shape.tpt;
+    const int ahead = two ? 1 : 2, c0 = two ? first_tile_count(a.shape, p) : m;
+#pragma unroll 1
+    for (int w = 0; w < (two ? 2 : 1); ++w)
+      if (!take_q(w)) return false;
+#pragma unroll 1
+    for (int i = -ahead; i < m; ++i) {
+      const bool more = i + ahead < m;
+      int v_buf = 0, k_buf = 0;
+#pragma unroll 1
+      for (int v = i >= 0; v >= (more ? 0 : 1); --v) {
+        int b;
+        if (!take(&b) || !load_kv(p.t0 + (v ? i : i + ahead), v, b)) return false;
+        if (v) v_buf = b; else k_buf = b;
+        if (v && !two) buf.give(b);
+      }
+      if (more && i + ahead == max(c0 - 1, 0)) buf.give(q_buf[0]);
+      if (two && i >= 0) buf.give(v_buf);
+      if (two && more && i + ahead == m - 1) buf.give(q_buf[1]);
+      if (more) buf.give(k_buf);
+    }
+    return true;
+  }
   __device__ void run() {
     Cursor cur_ = cursor(a, sh);
     while (cur_.next(&p)) {
       begin();
-      if (!piece_program(a.shape, p, *this)) return;
+      if (!fill()) return;
     }
   }
 };
@@ -561,14 +577,19 @@ struct Issuer {
     fence_proxy_async_smem();
     return true;
   }
-  __device__ bool take_q(int w) { return take(&q_buf[w]); }
+  __device__ bool take_q(int w) {
+    int b;
+    if (!take(&b)) return false;
+    if (w) q_buf[1] = b; else q_buf[0] = b;
+    return true;
+  }
   __device__ bool take_k(int) { return take(&k_buf); }
   __device__ bool take_v(int) { return take(&v_buf); }
   __device__ void give(int b) {
     if (elect_one()) tc_commit(&sh->empty[b]);
     buf.give(b);
   }
-  __device__ void give_q(int w) { give(q_buf[w]); }
+  __device__ void give_q(int w) { give(w ? q_buf[1] : q_buf[0]); }
   __device__ void give_k() { give(k_buf); }
   __device__ void give_v() { give(v_buf); }
   // Low words of the descriptors; the high word is the same for all.
@@ -576,8 +597,8 @@ struct Issuer {
     return ((tiles + b * Tile<DP>::kBytes) >> 4) | ((lead_bytes >> 4) << 16);
   }
   // S_w = Q K^T
-  __device__ void qk(int w) {
-    const uint32_t qd = desc(w && q2 ? q_buf[1] : q_buf[0], 16), kd = desc(k_buf, 16);
+  __device__ void qk(int w, int x) {
+    const uint32_t qd = desc(x ? q_buf[1] : q_buf[0], 16), kd = desc(k_buf, 16);
     const uint32_t s = tmem + w * 128;
     if (elect_one()) {
 #pragma unroll
@@ -588,7 +609,6 @@ struct Issuer {
       tc_commit(&sh->s_full[w]);
     }
   }
-  bool q2;  // the piece has two query tiles
   // The accumulators are free once the softmax warps have read the last piece's.
   __device__ bool begin_pv() {
     if (pieces > 0 && !wait(&sh->o_empty, (pieces - 1) & 1)) return false;
@@ -615,7 +635,6 @@ struct Issuer {
     Cursor cur = cursor(a, sh);
     AttendPiece p;
     while (cur.next(&p)) {
-      q2 = p.ntok > a.shape.tpt;
       if (!piece_program(a.shape, p, *this)) {
         // Instructions in flight end before tensor memory is given back.
         if (elect_one()) tc_commit(&sh->drain);

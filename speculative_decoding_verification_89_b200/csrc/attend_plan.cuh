@@ -19,15 +19,17 @@
 
 #ifdef __CUDACC__
 #define SPECV_HD __host__ __device__ __forceinline__
+#define SPECV_HD_CALL __host__ __device__ __noinline__
 #else
 #define SPECV_HD inline
+#define SPECV_HD_CALL inline
 #endif
 
 namespace specv {
 
 constexpr int kTileRows = 128;  // query rows of a tile
 constexpr int kTileKeys = 128;  // keys of a K/V tile
-constexpr int kUnitCost = 1;    // a unit's fixed cost, in K/V tiles
+constexpr int kUnitCost = 3;    // a unit's fixed cost, in K/V tiles
 
 // sum_{i=0}^{n-1} floor((a*i + b) / m) for n, a, b >= 0, m > 0: the lattice
 // points under a line, by Euclid's algorithm on (a, m).
@@ -99,7 +101,7 @@ struct AttendShape {
     return m * (b >> 7) + step_sum(m + s, 7 - log_w) - step_sum(s, 7 - log_w);
   }
   // Cost of units 0 .. u-1.
-  SPECV_HD long long cost_before(const AttendSeq& s, int u) const {
+  SPECV_HD_CALL long long cost_before(const AttendSeq& s, int u) const {
     const int all = units(s);
     long long c = (long long)u * kUnitCost;
     int full = u;  // units whose last token is (i + 1) * w - 1
@@ -185,7 +187,7 @@ struct AttendCursor {
           }
         }
       }
-      if (p->t0 < p->t1 || nt == 0) return true;
+      if (p->t0 < p->t1 || (nt == 0 && x0 == 0)) return true;
     }
     return false;
   }
