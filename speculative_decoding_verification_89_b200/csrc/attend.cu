@@ -40,12 +40,12 @@ constexpr float kSlack = 8.0f;    // log2 of the largest p~
 template <int DP>
 struct Tile {
   static constexpr int kBytes = 128 * DP * 2;
-  static constexpr int kCount = DP == 128 ? 7 : 13;
+  static constexpr int kCount = DP == 128 ? 7 : 8;
   static constexpr int kSmemTiles = kCount * kBytes;
 };
 
 struct Shared {
-  uint64_t full[13], empty[13], landed[13];
+  uint64_t full[8], empty[8], landed[8];
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t o_empty, swap, drain;
   uint32_t tmem;
@@ -197,24 +197,23 @@ __device__ __forceinline__ Cursor cursor(const AttendArgs& a, const Shared* sh) 
 // buffer on both sides; the barriers' phases follow from each buffer's uses.
 template <int N>
 struct Buffers {
-  uint64_t queue;
-  int count;
-  uint32_t phases;  // bit b: parity of buffer b's next use
-  __device__ Buffers() : queue(0), count(N), phases(0) {
+  uint32_t queue, end;  // end: bit position behind the last one
+  uint32_t phases;      // bit b: parity of buffer b's next use
+  __device__ Buffers() : queue(0), end(4 * N), phases(0) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) queue |= (uint64_t)i << (4 * i);
+    for (int i = 0; i < N; ++i) queue |= (uint32_t)i << (4 * i);
   }
-  __device__ int take(uint32_t* parity) {
+  __device__ __forceinline__ int take(uint32_t* parity) {
     const int b = (int)(queue & 15);
     queue >>= 4;
-    --count;
+    end -= 4;
     *parity = (phases >> b) & 1;
     phases ^= 1u << b;
     return b;
   }
-  __device__ void give(int b) {
-    queue |= (uint64_t)b << (4 * count);
-    ++count;
+  __device__ __forceinline__ void give(int b) {
+    queue |= (uint32_t)b << end;
+    end += 4;
   }
 };
 
@@ -552,6 +551,8 @@ struct Loader {
 // ---------------------------------------------------------------------------
 // Matrix instructions, issued by one lane of a warp
 // ---------------------------------------------------------------------------
+// One thread runs all of it: between two products it is what the tensor cores
+// wait for, so it makes no votes and no elections.
 template <typename T, int DP>
 struct Issuer {
   static constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
@@ -561,83 +562,71 @@ struct Issuer {
   Shared* sh;
   uint32_t tiles, tmem;
   Buffers<Tile<DP>::kCount> buf;
-  int q_buf[2], k_buf, v_buf;
+  int q0_buf, q1_buf, k_buf, v_buf;
   uint32_t p_ph;     // bit w: parity of p_full[w]
   uint32_t pieces;   // with K/V tiles
 
   __device__ Issuer(const AttendArgs& a_, Shared* s, uint32_t t, uint32_t m)
       : a(a_), sh(s), tiles(t), tmem(m), p_ph(0), pieces(0) {}
-  __device__ bool wait(uint64_t* bar, uint32_t ph) {
-    return __all_sync(0xffffffffu, wait_bar(bar, ph, sh, a.status));
+  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t ph) {
+    return wait_bar(bar, ph, sh, a.status);
   }
-  __device__ bool take(int* b) {
+  __device__ __forceinline__ bool take(int* b) {
     uint32_t ph;
     *b = buf.take(&ph);
-    if (!wait(&sh->full[*b], ph)) return false;
-    fence_proxy_async_smem();
-    return true;
+    return wait(&sh->full[*b], ph);
   }
-  __device__ bool take_q(int w) {
-    int b;
-    if (!take(&b)) return false;
-    if (w) q_buf[1] = b; else q_buf[0] = b;
-    return true;
-  }
-  __device__ bool take_k(int) { return take(&k_buf); }
-  __device__ bool take_v(int) { return take(&v_buf); }
-  __device__ void give(int b) {
-    if (elect_one()) tc_commit(&sh->empty[b]);
+  __device__ __forceinline__ bool take_q(int w) { return take(w ? &q1_buf : &q0_buf); }
+  __device__ __forceinline__ bool take_k(int) { return take(&k_buf); }
+  __device__ __forceinline__ bool take_v(int) { return take(&v_buf); }
+  __device__ __forceinline__ void give(int b) {
+    tc_commit(&sh->empty[b]);
     buf.give(b);
   }
-  __device__ void give_q(int w) { give(w ? q_buf[1] : q_buf[0]); }
-  __device__ void give_k() { give(k_buf); }
-  __device__ void give_v() { give(v_buf); }
+  __device__ __forceinline__ void give_q(int w) { give(w ? q1_buf : q0_buf); }
+  __device__ __forceinline__ void give_k() { give(k_buf); }
+  __device__ __forceinline__ void give_v() { give(v_buf); }
   // Low words of the descriptors; the high word is the same for all.
-  __device__ uint32_t desc(int b, uint32_t lead_bytes) const {
+  __device__ __forceinline__ uint32_t desc(int b, uint32_t lead_bytes) const {
     return ((tiles + b * Tile<DP>::kBytes) >> 4) | ((lead_bytes >> 4) << 16);
   }
   // S_w = Q K^T
-  __device__ void qk(int w, int x) {
-    const uint32_t qd = desc(x ? q_buf[1] : q_buf[0], 16), kd = desc(k_buf, 16);
+  __device__ __forceinline__ void qk(int w, int x) {
+    const uint32_t qd = desc(x ? q1_buf : q0_buf, 16), kd = desc(k_buf, 16);
     const uint32_t s = tmem + w * 128;
-    if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < DP / 16; ++k) {
-        const uint32_t off = (k >> 2) * (128 * 128 / 16) + (k & 3) * 2;
-        mma_ss(s, mma_sdesc(qd + off), mma_sdesc(kd + off), kIdescQK, k > 0);
-      }
-      tc_commit(&sh->s_full[w]);
+    for (int k = 0; k < DP / 16; ++k) {
+      const uint32_t off = (k >> 2) * (128 * 128 / 16) + (k & 3) * 2;
+      mma_ss(s, mma_sdesc(qd + off), mma_sdesc(kd + off), kIdescQK, k > 0);
     }
+    tc_commit(&sh->s_full[w]);
   }
   // The accumulators are free once the softmax warps have read the last piece's.
-  __device__ bool begin_pv() {
+  __device__ __forceinline__ bool begin_pv() {
     if (pieces > 0 && !wait(&sh->o_empty, (pieces - 1) & 1)) return false;
     ++pieces;
-    tc_fence_after();
     return true;
   }
   // O_w (+)= P_w V
-  __device__ bool pv(int w, bool first, bool last) {
+  __device__ __forceinline__ bool pv(int w, bool first, bool last) {
+    const uint32_t vd = desc(v_buf, 128 * 128);
+    const uint32_t s = tmem + w * 128, o = tmem + 256 + w * DP;
     if (!wait(&sh->p_full[w], (p_ph >> w) & 1)) return false;
     p_ph ^= 1u << w;
     tc_fence_after();
-    const uint32_t vd = desc(v_buf, 128 * 128);
-    const uint32_t s = tmem + w * 128, o = tmem + 256 + w * DP;
-    if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < kTileKeys / 16; ++k)
-        mma_ts(o, s + k * 8, mma_sdesc(vd + k * (16 * 128 / 16)), kIdescPV, k > 0 || !first);
-      if (last) tc_commit(&sh->o_full[w]);
-    }
+    for (int k = 0; k < kTileKeys / 16; ++k)
+      mma_ts(o, s + k * 8, mma_sdesc(vd + k * (16 * 128 / 16)), kIdescPV, k > 0 || !first);
+    if (last) tc_commit(&sh->o_full[w]);
     return true;
   }
-  __device__ void run() {
+  __device__ __forceinline__ void run() {
     Cursor cur = cursor(a, sh);
     AttendPiece p;
     while (cur.next(&p)) {
       if (!piece_program(a.shape, p, *this)) {
         // Instructions in flight end before tensor memory is given back.
-        if (elect_one()) tc_commit(&sh->drain);
+        tc_commit(&sh->drain);
         mbar_wait_bounded(&sh->drain, 0, kWaitLimitNs);
         return;
       }
@@ -963,8 +952,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     s.run();
   } else if (warp == 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    Issuer<T, DP> s(a, sh, tiles, tmem);
-    s.run();
+    if (elect_one()) {
+      Issuer<T, DP> s(a, sh, tiles, tmem);
+      s.run();
+    }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     Loader<DP> s(a, sh, tiles, tid - 9 * 32);
