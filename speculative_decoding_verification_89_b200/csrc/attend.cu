@@ -250,28 +250,47 @@ __device__ __forceinline__ bool piece_program(const AttendShape& shape, const At
                                               Side& side) {
   const int m = p.t1 - p.t0;
   if (m == 0) return true;  // rows that see nothing
-  const bool two = p.ntok > shape.tpt;
-  const int ahead = two ? 1 : 2, c0 = two ? first_tile_count(shape, p) : m;
+  if (!side.take_q(0)) return false;
+  if (p.ntok > shape.tpt) {
+    const int c0 = first_tile_count(shape, p);
+    if (!side.take_q(1)) return false;
 #pragma unroll 1
-  for (int w = 0; w < (two ? 2 : 1); ++w)
-    if (!side.take_q(w)) return false;
-#pragma unroll 1
-  for (int i = -ahead; i < m; ++i) {
-    const bool more = i + ahead < m;
-    if (i == 0 && !side.begin_pv()) return false;
-    if (i >= 0 && !side.take_v(i)) return false;
-    const int w0 = two ? 0 : i & 1, w1 = two ? 1 : w0;
-#pragma unroll 1
-    for (int w = w0; w <= w1; ++w) {
-      const int x = two ? w : 0;           // its query tile
-      const int count = x ? m : c0;        // K/V tiles that this one needs
-      if (i >= 0 && i < count && !side.pv(w, i < ahead, i + ahead >= count)) return false;
-      if (i >= 0 && w == w1) side.give_v();
+    for (int i = -1; i < m; ++i) {
+      const bool more = i + 1 < m;
+      if (i == 0 && !side.begin_pv()) return false;
+      if (i >= 0) {
+        if (!side.take_v(i)) return false;
+        if (i < c0 && !side.pv(0, i == 0, i + 1 == c0)) return false;
+      }
       if (more) {
-        if (w == w0 && !side.take_k(i + ahead)) return false;
-        if (i + ahead < count) side.qk(w, x);
-        if (i + ahead == max(count - 1, 0)) side.give_q(x);
-        if (w == w1) side.give_k();
+        if (!side.take_k(i + 1)) return false;
+        if (i + 1 < c0) side.qk(0, 0);
+        if (i + 1 == max(c0 - 1, 0)) side.give_q(0);
+      }
+      if (i >= 0) {
+        if (!side.pv(1, i == 0, !more)) return false;
+        side.give_v();
+      }
+      if (more) {
+        side.qk(1, 1);
+        if (i + 2 == m) side.give_q(1);
+        side.give_k();
+      }
+    }
+  } else {
+#pragma unroll 1
+    for (int i = -2; i < m; ++i) {
+      const int w = i & 1;
+      if (i == 0 && !side.begin_pv()) return false;
+      if (i >= 0) {
+        if (!side.take_v(i) || !side.pv(w, i < 2, i + 2 >= m)) return false;
+        side.give_v();
+      }
+      if (i + 2 < m) {
+        if (!side.take_k(i + 2)) return false;
+        side.qk(w, 0);
+        if (i + 3 == m) side.give_q(0);
+        side.give_k();
       }
     }
   }
