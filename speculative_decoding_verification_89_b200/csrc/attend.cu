@@ -44,7 +44,21 @@ struct Tile {
   static constexpr int kSmemTiles = kCount * kBytes;
 };
 
+// A piece as the scheduling warp (the third loading warp) passes it to the others.
+struct Msg {
+  AttendSeq s;
+  int b, h;
+  int t0, m;         // first K/V tile and number of tiles
+  int tok0, ntok;    // the unit's tokens within the sequence
+  int c0, c1;        // tiles of each accumulator
+  int two;           // two query tiles
+  int part;          // 0 whole, 1 a later part of its unit, 2 the first of several
+  int end;           // no piece: the run is over
+};
+constexpr int kMsgs = 4;
+
 struct Shared {
+  uint64_t msg_full[kMsgs], msg_empty[kMsgs];
   uint64_t full[8], empty[8], landed[8];
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t o_empty, swap, drain;
@@ -54,32 +68,39 @@ struct Shared {
   AttendSeq seq;      // the first unit's sequence
   int start[4];       // sequence, head, unit, cost taken of it
   long long run;      // cost of this CTA's run
+  Msg msg[kMsgs];
   float2 ml[2][kTileRows];
 };
 static_assert(Tile<128>::kSmemTiles + sizeof(Shared) <= 227 * 1024, "shared memory");
 
 // A wait on a barrier phase, bounded by kWaitCycles of the SM's clock (2 s at
-// 1.9 GHz; cheaper to read than the global timer). A wait that runs out (or another's
-// that did) ends the CTA's work.
+// 1.9 GHz; cheaper to read than the global timer). In assembly to stay a few
+// instructions long: it is in many places. A role whose wait runs out ends; the
+// others' waits then run out too.
 constexpr long long kWaitCycles = 3800000000ll;
-__device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity, Shared* sh,
-                                       int32_t* status) {
-  const long long t0 = clock64();
-  for (;;) {
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-    if (*(volatile int*)&sh->abort) return false;
-    if (clock64() - t0 > kWaitCycles) {
-      *(volatile int*)&sh->abort = 1;
-      set_status(status, SPEC_ETIMEOUT);
-      return false;
-    }
-  }
-}
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Shared* sh,
-                                         int32_t* status) {
-  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, sh, status);
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t"
+      ".reg .pred p, q;\n\t"
+      ".reg .b64 t, u;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE;\n\t"
+      "mov.u64 t, %%clock64;\n\t"
+      "AGAIN:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE;\n\t"
+      "mov.u64 u, %%clock64;\n\t"
+      "sub.s64 u, u, t;\n\t"
+      "setp.lt.s64 q, u, %3;\n\t"
+      "@q bra AGAIN;\n\t"
+      "DONE:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "l"(kWaitCycles)
+      : "memory");
+  return ok != 0;
 }
 
 // Sequence b, with what is invalid made empty.
@@ -226,6 +247,19 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
+// A role's place in the ring of messages. `read` copies the next one; the caller
+// then gives its slot back (one arrival per softmax warp, issuer and copying warp).
+struct MsgRing {
+  int i = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void step() {
+    if (++i == kMsgs) {
+      i = 0;
+      ph ^= 1;
+    }
+  }
+};
+
 // Tiles of a unit that its first 128-row tile needs (two-tile units).
 __device__ __forceinline__ int first_tile_count(const AttendShape& shape, const AttendPiece& p) {
   const int nt0 = shape.tiles_upto(p.s, p.tok0 + shape.tpt - 1);
@@ -246,13 +280,10 @@ __device__ __forceinline__ int first_tile_count(const AttendShape& shape, const 
 // (The loading warps' side is Loader::fill: the same takes and gives in the
 // same order, with one place that loads.)
 template <typename Side>
-__device__ __forceinline__ bool piece_program(const AttendShape& shape, const AttendPiece& p,
-                                              Side& side) {
-  const int m = p.t1 - p.t0;
+__device__ __forceinline__ bool piece_program(int m, bool two, int c0, Side& side) {
   if (m == 0) return true;  // rows that see nothing
   if (!side.take_q(0)) return false;
-  if (p.ntok > shape.tpt) {
-    const int c0 = first_tile_count(shape, p);
+  if (two) {
     if (!side.take_q(1)) return false;
 #pragma unroll 1
     for (int i = -1; i < m; ++i) {
@@ -307,7 +338,7 @@ __device__ __forceinline__ bool piece_program(const AttendShape& shape, const At
 // product: a weight of 0 times a NaN) and staged rows are put in their place.
 // A tile is full when all three warps have arrived. Pages that no box fits
 // are copied row by row by all three.
-template <int DP>
+template <int DP, bool kMends>
 struct Loader {
   static constexpr int kChunks = DP / 8;   // 16-byte chunks of a row
   const AttendArgs& a;
@@ -315,7 +346,7 @@ struct Loader {
   uint32_t tiles;     // shared address of the tiles
   int role, lane;     // 0-2: columns 0-63, columns 64-127, mending
   Buffers<Tile<DP>::kCount> buf;
-  AttendPiece p;
+  Msg p;
   int pooled;         // keys of the sequence in the pool (or packed rows)
   int q_buf[2];
   uint32_t issued;    // buffers filled at least once, by bit
@@ -327,13 +358,13 @@ struct Loader {
   __device__ Loader(const AttendArgs& a_, Shared* s, uint32_t t, int thread)
       : a(a_), sh(s), tiles(t), role(thread >> 5), lane(thread & 31), issued(0), land_ph(0) {}
   __device__ bool wait(uint64_t* bar, uint32_t ph) {
-    return __all_sync(0xffffffffu, wait_bar(bar, ph, sh, a.status));
+    return __all_sync(0xffffffffu, wait_bar(bar, ph));
   }
-  // After a wait that ran out: the copies in flight land before the CTA ends.
+  // The copies in flight land before the CTA ends, also after a wait that ran out.
   __device__ void drain() {
+#pragma unroll 1
     for (int b = 0; b < Tile<DP>::kCount; ++b)
-      if (issued >> b & 1)
-        mbar_wait_bounded(&sh->full[b], ((buf.phases >> b) & 1) ^ 1, kWaitLimitNs);
+      if (issued >> b & 1) wait_bar(&sh->full[b], ((buf.phases >> b) & 1) ^ 1);
   }
   __device__ bool take(int* b) {
     uint32_t ph;
@@ -353,7 +384,7 @@ struct Loader {
   __device__ bool copies() const { return role == 0 || (role == 1 && a.dim > 64); }
   __device__ void begin() {
     pooled = a.stage_k ? p.s.len - p.s.n : p.s.len;
-    if (!a.tables || !a.box_rows || p.t1 == p.t0) return;
+    if (kMends || !a.tables || !a.box_rows || p.m == 0) return;
     group = page_of(p.t0 * kTileKeys) >> 5;
     cur = entry(group * 32 + lane);
     next = entry(group * 32 + 32 + lane);
@@ -369,7 +400,7 @@ struct Loader {
     const uint32_t bytes = a.shape.tpt * a.group * 128;
     const uint32_t dst = tile(b) + role * (128 * 128);
     if (elect_one()) {
-      if (copies()) {
+      if (!kMends && copies()) {
         mbar_arrive_expect_tx(bar, bytes);
         tma_box4(dst, &a.map_q, role * 64, 0, p.h, tok0, bar);
       } else {
@@ -387,8 +418,12 @@ struct Loader {
     }
     const bool mend = (t + 1) * kTileKeys > pooled && (v || a.stage_k);
     uint64_t* bar = mend ? &sh->landed[b] : &sh->full[b];
-    if (role == 2 && mend) {
-      if (!mend_tile(t, v, b)) return false;
+    if constexpr (kMends) {
+      if (mend) {
+        if (!mend_tile(t, v, b)) return false;
+      } else if (elect_one()) {
+        mbar_arrive(&sh->full[b]);
+      }
     } else if (copies()) {
       if (elect_one()) {
         mbar_arrive_expect_tx(bar, 128 * 128);
@@ -533,10 +568,10 @@ struct Loader {
   }
   // The loads of a piece, in piece_program's order of takes and gives.
   __device__ bool fill() {
-    const int m = p.t1 - p.t0;
+    const int m = p.m;
     if (m == 0) return true;
-    const bool two = p.ntok > a.shape.tpt;
-    const int ahead = two ? 1 : 2, c0 = two ? first_tile_count(a.shape, p) : m;
+    const bool two = p.two;
+    const int ahead = two ? 1 : 2, c0 = two ? p.c0 : m;
 #pragma unroll 1
     for (int w = 0; w < (two ? 2 : 1); ++w)
       if (!take_q(w)) return false;
@@ -558,12 +593,77 @@ struct Loader {
     }
     return true;
   }
-  __device__ void run() {
-    Cursor cur_ = cursor(a, sh);
-    while (cur_.next(&p)) {
+  // The copying warps.
+  __device__ bool run() {
+    MsgRing ring;
+    for (;;) {
+      if (!wait(&sh->msg_full[ring.i], ring.ph)) return false;
+      p = sh->msg[ring.i];
+      __syncwarp();
+      if (p.end) return true;
+      if (lane == 0) mbar_arrive(&sh->msg_empty[ring.i]);
+      ring.step();
       begin();
-      if (!fill()) return;
+      if (!fill()) return false;
     }
+  }
+  // The third warp walks the CTA's run, two pieces ahead of the one that it mends:
+  // a message's slot is free once all have read the one four before it, for which
+  // every piece before that has to be mended.
+  __device__ bool schedule() {
+    Cursor cur_ = cursor(a, sh);
+    MsgRing out, in;
+    AttendRec rec = {};
+    int ahead = 0;
+    bool over = false;
+    for (;;) {
+      while (!over && ahead < 3) {
+        AttendPiece x;
+        over = !cur_.next(&x);
+        if (!wait(&sh->msg_empty[out.i], out.ph ^ 1)) return false;
+        if (lane == 0) {
+          Msg* q = &sh->msg[out.i];
+          q->end = over;
+          if (!over) {
+            const int m = x.t1 - x.t0;
+            const bool two = x.ntok > a.shape.tpt;
+            q->s = x.s;
+            q->b = x.b;
+            q->h = x.h;
+            q->t0 = x.t0;
+            q->m = m;
+            q->tok0 = x.tok0;
+            q->ntok = x.ntok;
+            q->two = two;
+            q->c0 = two ? first_tile_count(a.shape, x) : (m + 1) / 2;
+            q->c1 = two ? m : m / 2;
+            q->part = x.t0 > 0 ? 1 : x.t1 < x.nt ? 2 : 0;
+            if (x.t0 > 0) {
+              rec.first = 1;
+              rec.first_cont = x.t1 < x.nt;
+            } else if (x.t1 < x.nt) {
+              rec.head = 1;
+              rec.row0 = x.s.row0;
+              rec.tok0 = x.tok0;
+              rec.ntok = x.ntok;
+              rec.h = x.h;
+            }
+          }
+          mbar_arrive(&sh->msg_full[out.i]);
+        }
+        out.step();
+        ++ahead;
+      }
+      __syncwarp();
+      p = sh->msg[in.i];
+      in.step();
+      --ahead;
+      if (p.end) break;
+      begin();
+      if (!fill()) return false;
+    }
+    if (lane == 0) a.rec[blockIdx.x] = rec;
+    return true;
   }
 };
 
@@ -588,7 +688,7 @@ struct Issuer {
   __device__ Issuer(const AttendArgs& a_, Shared* s, uint32_t t, uint32_t m)
       : a(a_), sh(s), tiles(t), tmem(m), p_ph(0), pieces(0) {}
   __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t ph) {
-    return wait_bar(bar, ph, sh, a.status);
+    return wait_bar(bar, ph);
   }
   __device__ __forceinline__ bool take(int* b) {
     uint32_t ph;
@@ -639,17 +739,21 @@ struct Issuer {
     if (last) tc_commit(&sh->o_full[w]);
     return true;
   }
-  __device__ __forceinline__ void run() {
-    Cursor cur = cursor(a, sh);
-    AttendPiece p;
-    while (cur.next(&p)) {
-      if (!piece_program(a.shape, p, *this)) {
-        // Instructions in flight end before tensor memory is given back.
-        tc_commit(&sh->drain);
-        mbar_wait_bounded(&sh->drain, 0, kWaitLimitNs);
-        return;
-      }
+  __device__ __forceinline__ bool run() {
+    MsgRing ring;
+    for (;;) {
+      if (!wait(&sh->msg_full[ring.i], ring.ph)) break;
+      const Msg* q = &sh->msg[ring.i];
+      const int m = q->m, two = q->two, c0 = q->c0, end = q->end;
+      if (end) return true;
+      mbar_arrive(&sh->msg_empty[ring.i]);
+      ring.step();
+      if (!piece_program(m, two, c0, *this)) break;
     }
+    // Instructions in flight end before tensor memory is given back.
+    tc_commit(&sh->drain);
+    wait_bar(&sh->drain, 0);
+    return false;
   }
 };
 
@@ -706,7 +810,7 @@ struct Softmax {
   uint32_t s_ph, o_ph[2], x_ph;
 
   __device__ bool wait(uint64_t* bar, uint32_t ph) {
-    return __all_sync(0xffffffffu, wait_bar(bar, ph, sh, a.status));
+    return __all_sync(0xffffffffu, wait_bar(bar, ph));
   }
   __device__ void arrive(uint64_t* bar) {
     __syncwarp();
@@ -827,40 +931,30 @@ struct Softmax {
       }
     }
   }
-  __device__ void run() {
-    const AttendShape& shape = a.shape;
-    Cursor cur = cursor(a, sh);
-    AttendPiece p;
-    AttendRec rec = {};
-    while (cur.next(&p)) {
-      const int m_tiles = p.t1 - p.t0;
-      const bool two = p.ntok > shape.tpt;
-      const int base = two ? w * shape.tpt : 0;  // the tile's first token in the unit
-      const int ntok = min(shape.tpt, p.ntok - base);
-      const bool valid = tok < ntok;
+  __device__ bool run() {
+    MsgRing ring;
+    for (;;) {
+      if (!wait(&sh->msg_full[ring.i], ring.ph)) return false;
+      const Msg p = sh->msg[ring.i];
+      if (p.end) return true;
+      arrive(&sh->msg_empty[ring.i]);
+      ring.step();
+      const bool two = p.two;
+      const int tpt = a.shape.tpt;
+      const int base = two ? w * tpt : 0;  // the tile's first token in the unit
+      const bool valid = tok < min(tpt, p.ntok - base);
       const bool live = __any_sync(0xffffffffu, valid);
       const int limit = valid ? p.s.len - p.s.n + p.tok0 + base + tok : INT32_MAX;
       const int warp_limit = __reduce_min_sync(0xffffffffu, limit);
-      const int c0 = two ? first_tile_count(shape, p) : (m_tiles + 1) / 2;
-      const int c1 = two ? m_tiles : m_tiles / 2;
-      const int mine = w ? c1 : c0;
+      const int c0 = p.c0, c1 = p.c1, mine = w ? c1 : c0;
       float m = -INFINITY, l = 0.0f;
+#pragma unroll 1
       for (int i = 0; i < mine; ++i) {
         const int t = p.t0 + (two ? i : 2 * i + w);
-        if (!tile(t * kTileKeys, limit, warp_limit, live, valid, i == 0, m, l)) return;
+        if (!tile(t * kTileKeys, limit, warp_limit, live, valid, i == 0, m, l)) return false;
       }
-      if (p.t0 > 0) {
-        rec.first = 1;
-        rec.first_cont = p.t1 < p.nt;
-      } else if (p.t1 < p.nt) {
-        rec.head = 1;
-        rec.row0 = p.s.row0;
-        rec.tok0 = p.tok0;
-        rec.ntok = p.ntok;
-        rec.h = p.h;
-      }
-      const bool whole = p.t0 == 0 && p.t1 == p.nt;
-      const long long slot = 2 * blockIdx.x + (p.t0 > 0 ? 0 : 1);
+      const bool whole = p.part == 0;
+      const long long slot = 2 * blockIdx.x + (p.part == 1 ? 0 : 1);
       const long long prow = (slot * 2 + (two ? w : 0)) * kTileRows + row;
       const int r = p.s.row0 + p.tok0 + base + tok;
       const int qh = p.h * a.group + head;
@@ -870,17 +964,17 @@ struct Softmax {
       bool has0 = w == 0 && c0 > 0, has1 = w == 1 && c1 > 0;
       for (int x = 0; x < 2; ++x)
         if ((two ? x == w : true) && (x ? c1 : c0) > 0) {
-          if (!wait(&sh->o_full[x], o_ph[x])) return;
+          if (!wait(&sh->o_full[x], o_ph[x])) return false;
           o_ph[x] ^= 1;
         }
       if (!two) {  // both warpgroups hold part of every row: join, half the columns each
         sh->ml[w][row] = make_float2(m, l);
         arrive(&sh->swap);
-        if (!wait(&sh->swap, x_ph)) return;
+        if (!wait(&sh->swap, x_ph)) return false;
         x_ph ^= 1;
         const float2 u = sh->ml[w ^ 1][row];
         arrive(&sh->swap);
-        if (!wait(&sh->swap, x_ph)) return;
+        if (!wait(&sh->swap, x_ph)) return false;
         x_ph ^= 1;
         const float top = fmaxf(m, u.x);
         const float fm = weight(m, top), fu = weight(u.x, top);
@@ -896,7 +990,7 @@ struct Softmax {
       if (live) {
         tc_fence_after();
         if (whole) {
-          const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+          const float inv = l > 0.0f || l != l ? __fdividef(1.0f, l) : 0.0f;
           f0 *= inv;
           f1 *= inv;
         }
@@ -916,19 +1010,18 @@ struct Softmax {
           if (!whole) a.part_ml[prow] = make_float2(m, l);
           else if (a.lse)
             a.lse[(long long)r * a.q_heads + qh] =
-                l > 0.0f || l != l ? (float)((m + log2f(l)) * kLn2) : -INFINITY;
+                l > 0.0f || l != l ? (m + __log2f(l)) * (float)kLn2 : -INFINITY;
         }
         tc_fence_before();
       }
       // Both accumulators' phases are waited for before either is given back, so
       // no barrier can run two phases ahead of a waiting warp.
       if (two && (w ? c0 : c1) > 0) {
-        if (!wait(&sh->o_full[w ^ 1], o_ph[w ^ 1])) return;
+        if (!wait(&sh->o_full[w ^ 1], o_ph[w ^ 1])) return false;
         o_ph[w ^ 1] ^= 1;
       }
-      if (m_tiles > 0) arrive(&sh->o_empty);
+      if (p.m > 0) arrive(&sh->o_empty);
     }
-    if (threadIdx.x == 0) a.rec[blockIdx.x] = rec;
   }
 };
 
@@ -951,35 +1044,49 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     mbar_init(&sh->o_empty, 8);
     mbar_init(&sh->swap, 8);
     mbar_init(&sh->drain, 1);
+    for (int i = 0; i < kMsgs; ++i) {
+      mbar_init(&sh->msg_full[i], 1);
+      mbar_init(&sh->msg_empty[i], 8 + 1 + 2);
+    }
     sh->abort = 0;
     sh->run = 0;
     fence_barrier_init();
   }
-  pdl_begin();
   if (warp == 8) tmem_alloc(&sh->tmem, kTmemCols);
+  pdl_begin();
   tc_fence_before();
   find_run(a, sh);  // its barriers publish the above
   tc_fence_after();
   const uint32_t tiles = smem_u32(smem), tmem = sh->tmem;
   // Of the 384 * 168 registers of the launch, 208 to each softmax thread (a row's
   // 128 scores and their weights stay in registers), 88 to the others.
+  bool ok = true;
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int row = tid & 127, t = (int)a.by_group((uint32_t)row);
     Softmax<T, DP> s{a, sh, tmem + ((uint32_t)(warp & 3) << 21), warp >> 2, row, t,
                      row - t * a.group, 0, {0, 0}, 0};
-    s.run();
+    ok = s.run();
   } else if (warp == 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (elect_one()) {
       Issuer<T, DP> s(a, sh, tiles, tmem);
-      s.run();
+      ok = s.run();
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    Loader<DP> s(a, sh, tiles, tid - 9 * 32);
-    s.run();
-    if (*(volatile int*)&sh->abort) s.drain();
+    if (warp < 11) {
+      Loader<DP, false> s(a, sh, tiles, tid - 9 * 32);
+      ok = s.run();
+      s.drain();
+    } else {
+      Loader<DP, true> s(a, sh, tiles, tid - 9 * 32);
+      ok = s.schedule();
+    }
+  }
+  if (!ok) {
+    sh->abort = 1;
+    set_status(a.status, SPEC_ETIMEOUT);
   }
   __syncwarp();
   tc_fence_before();

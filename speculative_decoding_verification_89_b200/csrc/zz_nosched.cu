@@ -1,0 +1,1240 @@
+// Attention of packed query rows over packed or paged keys and values:
+//   o_i = sum_{j <= len-n+i} p_ij v_j,  p_ij = softmax_j(scale * q_i . k_j)
+// in one pass over the keys: with a running reference m and sum l,
+//   p~ = 2^(c s - m),  l += sum p~,  O += P~ V,  o = O / l,
+// c = scale * log2(e). The reference need not be the running maximum: it is
+// raised (and l, O scaled down) only when a maximum passes it by more than
+// 2^kSlack, so p~ stays below 2^kSlack and the scaling of O is rare.
+//
+// HiSpec (gist.science summary of arXiv 2510.01336), section 2
+// "Unterstuetzung fuer Batch-Inferenz" (paged attention with block tables) and
+// "Wiederverwendung von KV-Cache und versteckten Zustaenden" (K/V rows staged
+// while drafting, kept or dropped by the check).
+//
+// One persistent CTA per SM takes a run of K/V tiles (attend_plan.cuh). Of its
+// three warpgroups the first two are softmax warps, one thread per row of a
+// 128-row tile; in the third, one thread issues the matrix instructions
+// (tcgen05, accumulators in tensor memory) and three warps load. Scores S =
+// Q K^T of a tile land in tensor memory; its warpgroup turns them into P~ in
+// place (two-byte elements over the same columns), which the next instruction
+// reads as its left operand for O += P~ V. While one warpgroup works on its
+// scores, the tensor cores form the other's.
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "attend.cuh"
+#include "kernels.cuh"
+#include "tc05.cuh"
+
+namespace specv {
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kLoaders = 96;      // warps 9-11
+constexpr int kTmemCols = 512;    // S0 S1 O0 O1
+constexpr float kSlack = 8.0f;    // log2 of the largest p~
+
+// Buffers of one 128-row tile (Q, K or V) each; all of them serve all three.
+template <int DP>
+struct Tile {
+  static constexpr int kBytes = 128 * DP * 2;
+  static constexpr int kCount = DP == 128 ? 7 : 8;
+  static constexpr int kSmemTiles = kCount * kBytes;
+};
+
+// A piece as the scheduling warp (the third loading warp) passes it to the others.
+struct Msg {
+  AttendSeq s;
+  int b, h;
+  int t0, m;         // first K/V tile and number of tiles
+  int tok0, ntok;    // the unit's tokens within the sequence
+  int c0, c1;        // tiles of each accumulator
+  int two;           // two query tiles
+  int part;          // 0 whole, 1 a later part of its unit, 2 the first of several
+  int end;           // no piece: the run is over
+};
+constexpr int kMsgs = 4;
+
+struct Shared {
+  uint64_t msg_full[kMsgs], msg_empty[kMsgs];
+  uint64_t full[8], empty[8], landed[8];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t o_empty, swap, drain;
+  uint32_t tmem;
+  int abort;
+  long long warp_sum[kThreads / 32];
+  AttendSeq seq;      // the first unit's sequence
+  int start[4];       // sequence, head, unit, cost taken of it
+  long long run;      // cost of this CTA's run
+  Msg msg[kMsgs];
+  float2 ml[2][kTileRows];
+};
+static_assert(Tile<128>::kSmemTiles + sizeof(Shared) <= 227 * 1024, "shared memory");
+
+// A wait on a barrier phase, bounded by kWaitCycles of the SM's clock (2 s at
+// 1.9 GHz; cheaper to read than the global timer). In assembly to stay a few
+// instructions long: it is in many places. A role whose wait runs out ends; the
+// others' waits then run out too.
+constexpr long long kWaitCycles = 3800000000ll;
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t"
+      ".reg .pred p, q;\n\t"
+      ".reg .b64 t, u;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE;\n\t"
+      "mov.u64 t, %%clock64;\n\t"
+      "AGAIN:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE;\n\t"
+      "mov.u64 u, %%clock64;\n\t"
+      "sub.s64 u, u, t;\n\t"
+      "setp.lt.s64 q, u, %3;\n\t"
+      "@q bra AGAIN;\n\t"
+      "DONE:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "l"(kWaitCycles)
+      : "memory");
+  return ok != 0;
+}
+
+// Sequence b, with what is invalid made empty.
+struct SeqOf {
+  const AttendArgs* a;
+  __device__ AttendSeq operator()(int b) const { return get(b, nullptr); }
+  __device__ AttendSeq get(int b, int* bad) const {
+    AttendSeq s;
+    if (a->row_off) {
+      const int lo = a->row_off[b], hi = a->row_off[b + 1];
+      s.row0 = lo;
+      s.n = hi - lo;
+      if (lo < 0 || hi < lo || hi > a->T) {
+        s.row0 = s.n = 0;
+        if (bad) *bad = 1;
+      }
+    } else {
+      s.row0 = b * a->rows_per_seq;
+      s.n = a->rows_per_seq;
+    }
+    if (!a->tables) {
+      s.len = s.n;
+      return s;
+    }
+    s.len = a->seq_lens[b];
+    if (s.len < 0 || s.len > a->max_blocks * a->block_size || (a->stage_k && s.n > a->stage_rows)) {
+      s.len = 0;
+      if (bad) *bad = 1;
+    } else if (a->stage_k) {
+      s.len += s.n;
+    }
+    return s;
+  }
+};
+
+using Cursor = AttendCursor<SeqOf>;
+
+// a / b where it mostly fits 32 bits
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// The cost of a sequence under one head; of one unit without the general sum.
+__device__ __forceinline__ long long cost_of_head(const AttendShape& shape, const AttendSeq& s) {
+  if (s.n <= 0) return 0;
+  return s.n <= shape.w ? shape.tiles_upto(s, s.n - 1) + kUnitCost : shape.head_cost(s);
+}
+
+// Where this CTA's run of the cost line starts, into sh; all threads.
+__device__ __forceinline__ void find_run(const AttendArgs& a, Shared* sh) {
+  const SeqOf seq{&a};
+  const AttendShape& shape = a.shape;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.B + kThreads - 1) / kThreads;
+  const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+  long long sum = 0;
+  int bad = 0;
+  for (int b = b0; b < b1; ++b) {
+    const AttendSeq s = seq.get(b, &bad);
+    sum += cost_of_head(shape, s) * a.kv_heads;
+  }
+  if (bad && blockIdx.x == 0) set_status(a.status, SPEC_EDEVICE);
+  long long incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) sh->warp_sum[warp] = incl;
+  __syncthreads();
+  long long before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += sh->warp_sum[w];
+    total += sh->warp_sum[w];
+  }
+  const long long share = quotient(total + gridDim.x - 1, gridDim.x);
+  const long long from = share * blockIdx.x;
+  const long long to = min(total, from + share);
+  long long at = before + incl - sum;
+  if (from < to && from >= at && from < at + sum) {
+    for (int b = b0; b < b1; ++b) {
+      const AttendSeq s = seq(b);
+      const long long head = cost_of_head(shape, s);
+      if (from < at + head * a.kv_heads) {
+        const int h = (int)quotient(from - at, head);
+        const long long y = from - at - h * head;
+        int lo = 0, hi = shape.units(s) - 1;  // the unit u with cost_before(u) <= y
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (shape.cost_before(s, mid) <= y) lo = mid; else hi = mid - 1;
+        }
+        sh->seq = s;
+        sh->start[0] = b;
+        sh->start[1] = h;
+        sh->start[2] = lo;
+        sh->start[3] = (int)(lo ? y - shape.cost_before(s, lo) : y);
+        sh->run = to - from;
+        break;
+      }
+      at += head * a.kv_heads;
+    }
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ Cursor cursor(const AttendArgs& a, const Shared* sh) {
+  return Cursor(a.shape, SeqOf{&a}, a.B, a.kv_heads, sh->start[0], sh->start[1], sh->start[2],
+                sh->start[3], sh->run, sh->seq);
+}
+
+// The free buffers, in the order in which they will be given back: a queue of
+// 4-bit numbers, the next one lowest. The loading and the issuing warps step
+// through one program of takes and gives, so each n-th take gets the same
+// buffer on both sides; the barriers' phases follow from each buffer's uses.
+template <int N>
+struct Buffers {
+  uint32_t queue, end;  // end: bit position behind the last one
+  uint32_t phases;      // bit b: parity of buffer b's next use
+  __device__ Buffers() : queue(0), end(4 * N), phases(0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) queue |= (uint32_t)i << (4 * i);
+  }
+  __device__ __forceinline__ int take(uint32_t* parity) {
+    const int b = (int)(queue & 15);
+    queue >>= 4;
+    end -= 4;
+    *parity = (phases >> b) & 1;
+    phases ^= 1u << b;
+    return b;
+  }
+  __device__ __forceinline__ void give(int b) {
+    queue |= (uint32_t)b << end;
+    end += 4;
+  }
+};
+
+// One lane of a warp, the same for every call by the whole warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// A role's place in the ring of messages. `read` copies the next one; the caller
+// then gives its slot back (one arrival per softmax warp, issuer and copying warp).
+struct MsgRing {
+  int i = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void step() {
+    if (++i == kMsgs) {
+      i = 0;
+      ph ^= 1;
+    }
+  }
+};
+
+// Tiles of a unit that its first 128-row tile needs (two-tile units).
+__device__ __forceinline__ int first_tile_count(const AttendShape& shape, const AttendPiece& p) {
+  const int nt0 = shape.tiles_upto(p.s, p.tok0 + shape.tpt - 1);
+  return max(0, min(p.t1, nt0) - p.t0);
+}
+
+// The program of a piece. Two query tiles: both use each K
+// and V tile, the first may need fewer of them; K tiles are one ahead of the V
+// tiles. One query tile: the K/V tiles go to the two accumulators in turn, K
+// two ahead. Side:
+//   take_q(w), take_k(t), take_v(t): the next buffer, for query tile w, K or V
+//     tile t; give_q(w), give_k(), give_v(): it is free once what was issued is done;
+//   qk(w, x): scores of accumulator w with query tile x; begin_pv(): before the
+//     first pv; pv(w, first, last): weights times V.
+// Every step is written once: the code of both sides has to stay small enough
+// for the instruction cache beside the softmax warps' (unrolled by case it was
+// 376 KB, and the prompt of 8192 rows took 514 us).
+// (The loading warps' side is Loader::fill: the same takes and gives in the
+// same order, with one place that loads.)
+template <typename Side>
+__device__ __forceinline__ bool piece_program(int m, bool two, int c0, Side& side) {
+  if (m == 0) return true;  // rows that see nothing
+  if (!side.take_q(0)) return false;
+  if (two) {
+    if (!side.take_q(1)) return false;
+#pragma unroll 1
+    for (int i = -1; i < m; ++i) {
+      const bool more = i + 1 < m;
+      if (i == 0 && !side.begin_pv()) return false;
+      if (i >= 0) {
+        if (!side.take_v(i)) return false;
+        if (i < c0 && !side.pv(0, i == 0, i + 1 == c0)) return false;
+      }
+      if (more) {
+        if (!side.take_k(i + 1)) return false;
+        if (i + 1 < c0) side.qk(0, 0);
+        if (i + 1 == max(c0 - 1, 0)) side.give_q(0);
+      }
+      if (i >= 0) {
+        if (!side.pv(1, i == 0, !more)) return false;
+        side.give_v();
+      }
+      if (more) {
+        side.qk(1, 1);
+        if (i + 2 == m) side.give_q(1);
+        side.give_k();
+      }
+    }
+  } else {
+#pragma unroll 1
+    for (int i = -2; i < m; ++i) {
+      const int w = i & 1;
+      if (i == 0 && !side.begin_pv()) return false;
+      if (i >= 0) {
+        if (!side.take_v(i) || !side.pv(w, i < 2, i + 2 >= m)) return false;
+        side.give_v();
+      }
+      if (i + 2 < m) {
+        if (!side.take_k(i + 2)) return false;
+        side.qk(w, 0);
+        if (i + 3 == m) side.give_q(0);
+        side.give_k();
+      }
+    }
+  }
+  return true;
+}
+
+// ---------------------------------------------------------------------------
+// Loading: query rows, then K and V tiles in the order they are used
+// ---------------------------------------------------------------------------
+// Warp 9 copies columns 0-63 and warp 10 columns 64-127 of each tile with tiled
+// (TMA) copies: one for a query tile or 128 packed rows, one per page for the
+// pool. Warp 11 puts right what the copies of a sequence's last tiles cannot:
+// V rows past the keys are set to zero (what lies there must not reach a
+// product: a weight of 0 times a NaN) and staged rows are put in their place.
+// A tile is full when all three warps have arrived. Pages that no box fits
+// are copied row by row by all three.
+template <int DP, bool kMends>
+struct Loader {
+  static constexpr int kChunks = DP / 8;   // 16-byte chunks of a row
+  const AttendArgs& a;
+  Shared* sh;
+  uint32_t tiles;     // shared address of the tiles
+  int role, lane;     // 0-2: columns 0-63, columns 64-127, mending
+  Buffers<Tile<DP>::kCount> buf;
+  Msg p;
+  int pooled;         // keys of the sequence in the pool (or packed rows)
+  int q_buf[2];
+  uint32_t issued;    // buffers filled at least once, by bit
+  uint32_t land_ph;   // parity of each buffer's next use of `landed`
+  // Table entries of 32 consecutive pages, one per lane: the group that the K
+  // tiles have reached, the one before (V tiles follow) and the next one.
+  int group, cur, prev, next;
+
+  __device__ Loader(const AttendArgs& a_, Shared* s, uint32_t t, int thread)
+      : a(a_), sh(s), tiles(t), role(thread >> 5), lane(thread & 31), issued(0), land_ph(0) {}
+  __device__ bool wait(uint64_t* bar, uint32_t ph) {
+    return __all_sync(0xffffffffu, wait_bar(bar, ph));
+  }
+  // The copies in flight land before the CTA ends, also after a wait that ran out.
+  __device__ void drain() {
+#pragma unroll 1
+    for (int b = 0; b < Tile<DP>::kCount; ++b)
+      if (issued >> b & 1) wait_bar(&sh->full[b], ((buf.phases >> b) & 1) ^ 1);
+  }
+  __device__ bool take(int* b) {
+    uint32_t ph;
+    *b = buf.take(&ph);
+    if (!wait(&sh->empty[*b], ph ^ 1)) {
+      buf.phases ^= 1u << *b;  // not filled
+      return false;
+    }
+    issued |= 1u << *b;
+    return true;
+  }
+  __device__ uint32_t tile(int b) const { return tiles + b * Tile<DP>::kBytes; }
+  __device__ int entry(int page) const {
+    return page < a.max_blocks ? a.tables[(long long)p.b * a.max_blocks + page] : 0;
+  }
+  __device__ int page_of(int key) const { return (int)a.by_bs((uint32_t)key); }
+  __device__ bool copies() const { return role == 0 || (role == 1 && a.dim > 64); }
+  __device__ void begin() {
+    pooled = a.stage_k ? p.s.len - p.s.n : p.s.len;
+    if (kMends || !a.tables || !a.box_rows || p.m == 0) return;
+    group = page_of(p.t0 * kTileKeys) >> 5;
+    cur = entry(group * 32 + lane);
+    next = entry(group * 32 + 32 + lane);
+    prev = 0;
+  }
+  // This warp's columns of query tile w: rows (token, head of the group).
+  __device__ bool take_q(int w) {
+    int b;
+    if (!take(&b)) return false;
+    if (w) q_buf[1] = b; else q_buf[0] = b;
+    uint64_t* bar = &sh->full[b];
+    const int tok0 = p.s.row0 + p.tok0 + w * a.shape.tpt;
+    const uint32_t bytes = a.shape.tpt * a.group * 128;
+    const uint32_t dst = tile(b) + role * (128 * 128);
+    if (elect_one()) {
+      if (!kMends && copies()) {
+        mbar_arrive_expect_tx(bar, bytes);
+        tma_box4(dst, &a.map_q, role * 64, 0, p.h, tok0, bar);
+      } else {
+        mbar_arrive(bar);
+      }
+    }
+    return true;
+  }
+  // K (v = 0) or V (v = 1) rows of tile t of the piece's sequence.
+  __device__ bool load_kv(int t, int v, int b) {
+    if (!a.box_rows) {
+      load_rows(t, v, tile(b));
+      if (elect_one()) mbar_arrive(&sh->full[b]);
+      return true;
+    }
+    const bool mend = (t + 1) * kTileKeys > pooled && (v || a.stage_k);
+    uint64_t* bar = mend ? &sh->landed[b] : &sh->full[b];
+    if constexpr (kMends) {
+      if (mend) {
+        if (!mend_tile(t, v, b)) return false;
+      } else if (elect_one()) {
+        mbar_arrive(&sh->full[b]);
+      }
+    } else if (copies()) {
+      if (elect_one()) {
+        mbar_arrive_expect_tx(bar, 128 * 128);
+        if (mend) mbar_arrive(&sh->full[b]);
+      }
+      load_boxes(t, v, tile(b) + role * (128 * 128), bar);
+    } else if (elect_one()) {
+      if (mend) mbar_arrive(&sh->landed[b]);
+      mbar_arrive(&sh->full[b]);
+    }
+    if (mend) land_ph ^= 1u << b;
+    return true;
+  }
+  template <int kBoxes>
+  __device__ void page_boxes(const void* map, uint32_t dst, int first, int row, int id,
+                             uint64_t* bar) {
+    int from[kBoxes];
+#pragma unroll
+    for (int i = 0; i < kBoxes; ++i) from[i] = __shfl_sync(0xffffffffu, id, first + i);
+    if (elect_one()) {
+#pragma unroll
+      for (int i = 0; i < kBoxes; ++i)
+        tma_box4(dst + i * (kTileKeys / kBoxes) * 128, map, role * 64, p.h, row, from[i], bar);
+    }
+  }
+  __device__ void load_boxes(int t, int v, uint32_t dst, uint64_t* bar) {
+    const void* map = v ? &a.map_v : &a.map_k;
+    if (!a.tables) {
+      if (elect_one()) tma_box3(dst, map, role * 64, p.h, p.s.row0 + t * kTileKeys, bar);
+      return;
+    }
+    const int page = page_of(t * kTileKeys), g = page >> 5;
+    if (!v && g != group) {
+      prev = cur;
+      cur = next;
+      group = g;
+      next = entry(g * 32 + 32 + lane);
+    }
+    int id = g == group ? cur : prev;
+    const int row = t * kTileKeys - page * a.block_size;  // not 0 in a page larger than a tile
+    const int boxes = kTileKeys / a.box_rows;
+    const bool held = (g * 32 + lane) * (long long)a.block_size < pooled;
+    if (!held || id < 0 || id >= a.num_blocks) {
+      if (held && (unsigned)(lane - (page & 31)) < (unsigned)boxes)
+        set_status(a.status, SPEC_EDEVICE);
+      id = a.num_blocks;  // outside the tensor: zeros
+    }
+    if (boxes == 8) {  // pages of 16 rows: the numbers first, then all copies in a row
+      page_boxes<8>(map, dst, page & 31, row, id, bar);
+      return;
+    }
+#pragma unroll 1
+    for (int i = 0; i < boxes; ++i)
+      page_boxes<1>(map, dst + i * a.box_rows * 128, (page & 31) + i, row, id, bar);
+  }
+  __device__ uint32_t chunk_addr(uint32_t tile, int row, int c) const {
+    return tile + (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+  }
+  // Warp 11, once the copies have landed: staged rows to their places, zeros
+  // in the V rows past the keys that the copies may have filled.
+  __device__ bool mend_tile(int t, int v, int b) {
+    constexpr int kRows = 32 / kChunks;  // rows of a step
+    constexpr int kAhead = 4;
+    const int c = lane % kChunks, key0 = t * kTileKeys;
+    const int first = max(0, pooled - key0);             // first row not from the pool
+    const int end = min(kTileKeys, p.s.len - key0);      // first row past the keys
+    const int staged = a.stage_k ? max(0, end - first) : 0;
+    const unsigned char* src = nullptr;
+    if (staged)
+      src = (v ? a.stage_v : a.stage_k) + p.b * a.stage_seq +
+            (long long)(key0 + first - pooled) * a.stage_row + ((long long)p.h * a.dim + c * 8) * 2;
+    const uint32_t dst = tile(b);
+    uint4 x[kAhead];
+    const int r0 = lane / kChunks;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int r = r0 + i * kRows;
+      x[i] = r < staged && c * 8 < a.dim
+                 ? __ldg(reinterpret_cast<const uint4*>(src + r * a.stage_row))
+                 : make_uint4(0, 0, 0, 0);
+    }
+    if (!wait(&sh->landed[b], (land_ph >> b) & 1)) return false;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int r = r0 + i * kRows;
+      if (r < staged) st_shared16(chunk_addr(dst, first + r, c), x[i]);
+    }
+#pragma unroll 1
+    for (int r = r0 + kAhead * kRows; r < staged; r += kRows)
+      st_shared16(chunk_addr(dst, first + r, c),
+                  c * 8 < a.dim ? __ldg(reinterpret_cast<const uint4*>(src + r * a.stage_row))
+                                : make_uint4(0, 0, 0, 0));
+    if (v) {
+      int stop = kTileKeys;  // pages past the last are zeros already
+      if (a.tables) {
+        const int last = pooled > 0 ? page_of(pooled - 1) + 1 : 0;
+        stop = (int)min((long long)kTileKeys, (long long)last * a.block_size - key0);
+      }
+#pragma unroll 1
+      for (int r = first + staged + r0; r < stop; r += kRows)
+        st_shared16(chunk_addr(dst, r, c), make_uint4(0, 0, 0, 0));
+    }
+    fence_proxy_async_smem();
+    if (elect_one_after_sync()) mbar_arrive(&sh->full[b]);
+    return true;
+  }
+  __device__ void load_rows(int t, int v, uint32_t dst) {
+    constexpr int kStep = kLoaders / kChunks;
+    const int thread = role * 32 + lane, c = thread % kChunks;
+    const long long col = ((long long)p.h * a.dim + c * 8) * 2;
+    const unsigned char* base = v ? a.v : a.k;
+    const long long ld = v ? a.ld_v : a.ld_k;
+    const int32_t* table = a.tables + (long long)p.b * a.max_blocks;
+    bool bad = false;
+#pragma unroll 2
+    for (int r = thread / kChunks; r < kTileKeys; r += kStep) {
+      const int key = t * kTileKeys + r;
+      bool ok = key < p.s.len && c * 8 < a.dim;
+      const unsigned char* src = base;
+      if (key < pooled) {
+        const int blk = page_of(key);
+        int id = ok ? table[blk] : 0;
+        if (id < 0 || id >= a.num_blocks) {
+          bad = true;
+          ok = false;
+          id = 0;
+        }
+        src = base + id * a.page_bytes + (key - blk * a.block_size) * ld + col;
+      } else if (ok) {
+        src = (v ? a.stage_v : a.stage_k) + p.b * a.stage_seq + (key - pooled) * a.stage_row + col;
+      }
+      cp_async16(chunk_addr(dst, r, c), src, ok ? 16u : 0u);
+    }
+    if (bad) set_status(a.status, SPEC_EDEVICE);
+    cp_async_wait_all();
+    fence_proxy_async_smem();
+    __syncwarp();
+  }
+  __device__ bool elect_one_after_sync() {
+    __syncwarp();
+    return elect_one();
+  }
+  // The loads of a piece, in piece_program's order of takes and gives.
+  __device__ bool fill() {
+    const int m = p.m;
+    if (m == 0) return true;
+    const bool two = p.two;
+    const int ahead = two ? 1 : 2, c0 = two ? p.c0 : m;
+#pragma unroll 1
+    for (int w = 0; w < (two ? 2 : 1); ++w)
+      if (!take_q(w)) return false;
+#pragma unroll 1
+    for (int i = -ahead; i < m; ++i) {
+      const bool more = i + ahead < m;
+      int v_buf = 0, k_buf = 0;
+#pragma unroll 1
+      for (int v = i >= 0; v >= (more ? 0 : 1); --v) {
+        int b;
+        if (!take(&b) || !load_kv(p.t0 + (v ? i : i + ahead), v, b)) return false;
+        if (v) v_buf = b; else k_buf = b;
+        if (v && !two) buf.give(b);
+      }
+      if (more && i + ahead == max(c0 - 1, 0)) buf.give(q_buf[0]);
+      if (two && i >= 0) buf.give(v_buf);
+      if (two && more && i + ahead == m - 1) buf.give(q_buf[1]);
+      if (more) buf.give(k_buf);
+    }
+    return true;
+  }
+  // The copying warps.
+  __device__ bool run() {
+    MsgRing ring;
+    for (;;) {
+      if (!wait(&sh->msg_full[ring.i], ring.ph)) return false;
+      p = sh->msg[ring.i];
+      __syncwarp();
+      if (p.end) return true;
+      if (lane == 0) mbar_arrive(&sh->msg_empty[ring.i]);
+      ring.step();
+      begin();
+      if (!fill()) return false;
+    }
+  }
+  // The third warp walks the CTA's run, two pieces ahead of the one that it mends:
+  // a message's slot is free once all have read the one four before it, for which
+  // every piece before that has to be mended.
+  __device__ bool schedule() {
+    Cursor cur_ = cursor(a, sh);
+    MsgRing out, in;
+    AttendRec rec = {};
+    int ahead = 0;
+    bool over = false;
+    for (;;) {
+      while (!over && ahead < 3) {
+        AttendPiece x;
+        over = !cur_.next(&x);
+        if (!wait(&sh->msg_empty[out.i], out.ph ^ 1)) return false;
+        if (lane == 0) {
+          Msg* q = &sh->msg[out.i];
+          q->end = over;
+          if (!over) {
+            const int m = x.t1 - x.t0;
+            const bool two = x.ntok > a.shape.tpt;
+            q->s = x.s;
+            q->b = x.b;
+            q->h = x.h;
+            q->t0 = x.t0;
+            q->m = m;
+            q->tok0 = x.tok0;
+            q->ntok = x.ntok;
+            q->two = two;
+            q->c0 = two ? first_tile_count(a.shape, x) : (m + 1) / 2;
+            q->c1 = two ? m : m / 2;
+            q->part = x.t0 > 0 ? 1 : x.t1 < x.nt ? 2 : 0;
+            if (x.t0 > 0) {
+              rec.first = 1;
+              rec.first_cont = x.t1 < x.nt;
+            } else if (x.t1 < x.nt) {
+              rec.head = 1;
+              rec.row0 = x.s.row0;
+              rec.tok0 = x.tok0;
+              rec.ntok = x.ntok;
+              rec.h = x.h;
+            }
+          }
+          mbar_arrive(&sh->msg_full[out.i]);
+        }
+        out.step();
+        ++ahead;
+      }
+      __syncwarp();
+      p = sh->msg[in.i];
+      in.step();
+      --ahead;
+      if (p.end) break;
+      begin();
+      if (!fill()) return false;
+    }
+    if (lane == 0) a.rec[blockIdx.x] = rec;
+    return true;
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Matrix instructions, issued by one lane of a warp
+// ---------------------------------------------------------------------------
+// One thread runs all of it: between two products it is what the tensor cores
+// wait for, so it makes no votes and no elections.
+template <typename T, int DP>
+struct Issuer {
+  static constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
+  static constexpr uint32_t kIdescQK = mma_idesc(kBf, 128, 128, false);
+  static constexpr uint32_t kIdescPV = mma_idesc(kBf, 128, DP, true);
+  const AttendArgs& a;
+  Shared* sh;
+  uint32_t tiles, tmem;
+  Buffers<Tile<DP>::kCount> buf;
+  int q0_buf, q1_buf, k_buf, v_buf;
+  uint32_t p_ph;     // bit w: parity of p_full[w]
+  uint32_t pieces;   // with K/V tiles
+
+  __device__ Issuer(const AttendArgs& a_, Shared* s, uint32_t t, uint32_t m)
+      : a(a_), sh(s), tiles(t), tmem(m), p_ph(0), pieces(0) {}
+  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t ph) {
+    return wait_bar(bar, ph);
+  }
+  __device__ __forceinline__ bool take(int* b) {
+    uint32_t ph;
+    *b = buf.take(&ph);
+    return wait(&sh->full[*b], ph);
+  }
+  __device__ __forceinline__ bool take_q(int w) { return take(w ? &q1_buf : &q0_buf); }
+  __device__ __forceinline__ bool take_k(int) { return take(&k_buf); }
+  __device__ __forceinline__ bool take_v(int) { return take(&v_buf); }
+  __device__ __forceinline__ void give(int b) {
+    tc_commit(&sh->empty[b]);
+    buf.give(b);
+  }
+  __device__ __forceinline__ void give_q(int w) { give(w ? q1_buf : q0_buf); }
+  __device__ __forceinline__ void give_k() { give(k_buf); }
+  __device__ __forceinline__ void give_v() { give(v_buf); }
+  // Low words of the descriptors; the high word is the same for all.
+  __device__ __forceinline__ uint32_t desc(int b, uint32_t lead_bytes) const {
+    return ((tiles + b * Tile<DP>::kBytes) >> 4) | ((lead_bytes >> 4) << 16);
+  }
+  // S_w = Q K^T
+  __device__ __forceinline__ void qk(int w, int x) {
+    const uint32_t qd = desc(x ? q1_buf : q0_buf, 16), kd = desc(k_buf, 16);
+    const uint32_t s = tmem + w * 128;
+#pragma unroll
+    for (int k = 0; k < DP / 16; ++k) {
+      const uint32_t off = (k >> 2) * (128 * 128 / 16) + (k & 3) * 2;
+      mma_ss(s, mma_sdesc(qd + off), mma_sdesc(kd + off), kIdescQK, k > 0);
+    }
+    tc_commit(&sh->s_full[w]);
+  }
+  // The accumulators are free once the softmax warps have read the last piece's.
+  __device__ __forceinline__ bool begin_pv() {
+    if (pieces > 0 && !wait(&sh->o_empty, (pieces - 1) & 1)) return false;
+    ++pieces;
+    return true;
+  }
+  // O_w (+)= P_w V
+  __device__ __forceinline__ bool pv(int w, bool first, bool last) {
+    const uint32_t vd = desc(v_buf, 128 * 128);
+    const uint32_t s = tmem + w * 128, o = tmem + 256 + w * DP;
+    if (!wait(&sh->p_full[w], (p_ph >> w) & 1)) return false;
+    p_ph ^= 1u << w;
+    tc_fence_after();
+#pragma unroll
+    for (int k = 0; k < kTileKeys / 16; ++k)
+      mma_ts(o, s + k * 8, mma_sdesc(vd + k * (16 * 128 / 16)), kIdescPV, k > 0 || !first);
+    if (last) tc_commit(&sh->o_full[w]);
+    return true;
+  }
+  __device__ __forceinline__ bool run() {
+    MsgRing ring;
+    for (;;) {
+      if (!wait(&sh->msg_full[ring.i], ring.ph)) break;
+      const Msg* q = &sh->msg[ring.i];
+      const int m = q->m, two = q->two, c0 = q->c0, end = q->end;
+      if (end) return true;
+      mbar_arrive(&sh->msg_empty[ring.i]);
+      ring.step();
+      if (!piece_program(m, two, c0, *this)) break;
+    }
+    // Instructions in flight end before tensor memory is given back.
+    tc_commit(&sh->drain);
+    wait_bar(&sh->drain, 0);
+    return false;
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Softmax and output, one thread per row
+// ---------------------------------------------------------------------------
+template <typename T> struct Pack;
+template <> struct Pack<__nv_bfloat16> {
+  static __device__ __forceinline__ uint32_t two(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
+};
+template <> struct Pack<__half> {
+  static __device__ __forceinline__ uint32_t two(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
+};
+
+// Two fp32 operations per instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ float weight(float m, float ref) {
+  return m == -INFINITY ? 0.0f : ex2(m - ref);
+}
+
+template <typename T, int DP>
+struct Softmax {
+  const AttendArgs& a;
+  Shared* sh;
+  uint32_t tmem;    // with this warp's lanes
+  int w, row;       // warpgroup, row of the tile
+  int tok, head;    // row's token within a tile and query head within the group
+  uint32_t s_ph, o_ph[2], x_ph;
+
+  __device__ bool wait(uint64_t* bar, uint32_t ph) {
+    return __all_sync(0xffffffffu, wait_bar(bar, ph));
+  }
+  __device__ void arrive(uint64_t* bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+  }
+  // Scores of one tile to p~; m is the reference and l the sum, both of this row.
+  __device__ bool tile(int key0, int limit, int warp_limit, bool live, bool valid, bool first,
+                       float& m, float& l) {
+    if (!wait(&sh->s_full[w], s_ph)) return false;
+    s_ph ^= 1;
+    if (live) {
+      tc_fence_after();
+      uint32_t s[128];
+      const uint32_t col = tmem + w * 128;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tmem_ld32(col + 32 * i, s, 32 * i);
+      tmem_wait_ld(s);
+      if (key0 + kTileKeys - 1 > warp_limit) {
+        const int lim = limit - key0;
+#pragma unroll
+        for (int i = 0; i < 128; ++i)
+          if (i > lim) s[i] = 0xff800000u;
+      }
+      float mx[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(s[i]);
+#pragma unroll
+      for (int i = 4; i < 124; i += 8)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          mx[j] = fmaxf(fmaxf(mx[j], __uint_as_float(s[i + j])), __uint_as_float(s[i + 4 + j]));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], __uint_as_float(s[124 + j]));
+      const float top =
+          fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+      const bool raise = valid && (top > m + kSlack || (m == -INFINITY && top > m));
+      if (__any_sync(0xffffffffu, raise)) {
+        const float f = weight(m, fmaxf(m, top));
+        m = fmaxf(m, top);
+        l *= f;
+        if (!first) {  // the products up to the last tile's are in O
+#pragma unroll 1
+          for (int c = 0; c < DP; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(tmem + 256 + w * DP + c, o, 0);
+            tmem_wait_ld(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st32(tmem + 256 + w * DP + c, o, 0);
+          }
+        }
+      }
+      const float ref = m == -INFINITY ? 0.0f : m;
+      const uint64_t c2 = pair(a.scale_log2, a.scale_log2), r2 = pair(-ref, -ref);
+      uint64_t sum[2] = {0, 0};
+#pragma unroll
+      for (int i = 0; i < 128; i += 64) {
+        uint32_t p[32];
+#pragma unroll
+        for (int j = 0; j < 64; j += 2) {
+          float e0, e1;
+          unpair(fma2(pair(__uint_as_float(s[i + j]), __uint_as_float(s[i + j + 1])), c2, r2), e0,
+                 e1);
+          e0 = ex2(e0);
+          e1 = ex2(e1);
+          sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], pair(e0, e1));
+          p[j / 2] = Pack<T>::two(e0, e1);
+        }
+        tmem_st32(col + i / 2, p, 0);
+      }
+      float l0, l1;
+      unpair(add2(sum[0], sum[1]), l0, l1);
+      l += l0 + l1;
+      tmem_wait_st();
+      tc_fence_before();
+    }
+    arrive(&sh->p_full[w]);
+    return true;
+  }
+  // Columns [c0, c0 + 32) of f0 * O0 + f1 * O1; all lanes. A factor of 0 drops its
+  // part whatever it holds (rows that saw no key there, beside values not finite).
+  __device__ void read_o(int c0, bool has0, float f0, bool has1, float f1, float (&o)[32]) {
+    uint32_t x[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+    if (has0) {
+      tmem_ld32(tmem + 256 + c0, x, 0);
+      tmem_wait_ld(x);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = f0 == 0.0f ? 0.0f : f0 * __uint_as_float(x[i]);
+    }
+    if (has1) {
+      tmem_ld32(tmem + 256 + DP + c0, x, 0);
+      tmem_wait_ld(x);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = f1 == 0.0f ? o[i] : fmaf(f1, __uint_as_float(x[i]), o[i]);
+    }
+  }
+  // A thread's 32 columns; 32-byte sectors where the rows begin on them.
+  __device__ void write_out(unsigned char* dst, int c0, const float (&o)[32]) {
+    uint32_t x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = Pack<T>::two(o[2 * i], o[2 * i + 1]);
+#pragma unroll
+    for (int i = 0; i < 16; i += 8) {
+      unsigned char* d = dst + (c0 + 2 * i) * 2;
+      if (a.out_sectors) {
+        if (c0 + 2 * i < a.dim)
+          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d),
+                       "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3]), "r"(x[i + 4]),
+                       "r"(x[i + 5]), "r"(x[i + 6]), "r"(x[i + 7])
+                       : "memory");
+      } else {
+        if (c0 + 2 * i < a.dim)
+          *reinterpret_cast<uint4*>(d) = make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+        if (c0 + 2 * i + 8 < a.dim)
+          *reinterpret_cast<uint4*>(d + 16) = make_uint4(x[i + 4], x[i + 5], x[i + 6], x[i + 7]);
+      }
+    }
+  }
+  __device__ bool run() {
+    MsgRing ring;
+    for (;;) {
+      if (!wait(&sh->msg_full[ring.i], ring.ph)) return false;
+      const Msg p = sh->msg[ring.i];
+      if (p.end) return true;
+      arrive(&sh->msg_empty[ring.i]);
+      ring.step();
+      const bool two = p.two;
+      const int tpt = a.shape.tpt;
+      const int base = two ? w * tpt : 0;  // the tile's first token in the unit
+      const bool valid = tok < min(tpt, p.ntok - base);
+      const bool live = __any_sync(0xffffffffu, valid);
+      const int limit = valid ? p.s.len - p.s.n + p.tok0 + base + tok : INT32_MAX;
+      const int warp_limit = __reduce_min_sync(0xffffffffu, limit);
+      const int c0 = p.c0, c1 = p.c1, mine = w ? c1 : c0;
+      float m = -INFINITY, l = 0.0f;
+#pragma unroll 1
+      for (int i = 0; i < mine; ++i) {
+        const int t = p.t0 + (two ? i : 2 * i + w);
+        if (!tile(t * kTileKeys, limit, warp_limit, live, valid, i == 0, m, l)) return false;
+      }
+      const bool whole = p.part == 0;
+      const long long slot = 2 * blockIdx.x + (p.part == 1 ? 0 : 1);
+      const long long prow = (slot * 2 + (two ? w : 0)) * kTileRows + row;
+      const int r = p.s.row0 + p.tok0 + base + tok;
+      const int qh = p.h * a.group + head;
+      unsigned char* dst = a.out + r * a.ld_out + (long long)qh * a.dim * 2;
+      float f0 = w == 0 ? 1.0f : 0.0f, f1 = 1.0f - f0;
+      int from = 0, to = DP;
+      bool has0 = w == 0 && c0 > 0, has1 = w == 1 && c1 > 0;
+      for (int x = 0; x < 2; ++x)
+        if ((two ? x == w : true) && (x ? c1 : c0) > 0) {
+          if (!wait(&sh->o_full[x], o_ph[x])) return false;
+          o_ph[x] ^= 1;
+        }
+      if (!two) {  // both warpgroups hold part of every row: join, half the columns each
+        sh->ml[w][row] = make_float2(m, l);
+        arrive(&sh->swap);
+        if (!wait(&sh->swap, x_ph)) return false;
+        x_ph ^= 1;
+        const float2 u = sh->ml[w ^ 1][row];
+        arrive(&sh->swap);
+        if (!wait(&sh->swap, x_ph)) return false;
+        x_ph ^= 1;
+        const float top = fmaxf(m, u.x);
+        const float fm = weight(m, top), fu = weight(u.x, top);
+        f0 = w ? fu : fm;
+        f1 = w ? fm : fu;
+        l = fm * l + fu * u.y;
+        m = top;
+        has0 = c0 > 0;
+        has1 = c1 > 0;
+        from = w * (DP / 2);
+        to = from + DP / 2;
+      }
+      if (live) {
+        tc_fence_after();
+        if (whole) {
+          const float inv = l > 0.0f || l != l ? __fdividef(1.0f, l) : 0.0f;
+          f0 *= inv;
+          f1 *= inv;
+        }
+#pragma unroll 1
+        for (int c = from; c < to; c += 32) {
+          float o[32];
+          read_o(c, has0, f0, has1, f1, o);
+          if (valid && whole) write_out(dst, c, o);
+          if (valid && !whole) {
+            float4* po = reinterpret_cast<float4*>(a.part_o + prow * DP + c);
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              po[i / 4] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          }
+        }
+        if (valid && (two || w == 0)) {
+          if (!whole) a.part_ml[prow] = make_float2(m, l);
+          else if (a.lse)
+            a.lse[(long long)r * a.q_heads + qh] =
+                l > 0.0f || l != l ? (m + __log2f(l)) * (float)kLn2 : -INFINITY;
+        }
+        tc_fence_before();
+      }
+      // Both accumulators' phases are waited for before either is given back, so
+      // no barrier can run two phases ahead of a waiting warp.
+      if (two && (w ? c0 : c1) > 0) {
+        if (!wait(&sh->o_full[w ^ 1], o_ph[w ^ 1])) return false;
+        o_ph[w ^ 1] ^= 1;
+      }
+      if (p.m > 0) arrive(&sh->o_empty);
+    }
+  }
+};
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_constant__ AttendArgs a) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  Shared* sh = reinterpret_cast<Shared*>(smem + Tile<DP>::kSmemTiles);
+  const int tid = threadIdx.x, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < Tile<DP>::kCount; ++i) {
+      mbar_init(&sh->full[i], 3);
+      mbar_init(&sh->empty[i], 1);
+      mbar_init(&sh->landed[i], 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->s_full[i], 1);
+      mbar_init(&sh->p_full[i], 4);
+      mbar_init(&sh->o_full[i], 1);
+    }
+    mbar_init(&sh->o_empty, 8);
+    mbar_init(&sh->swap, 8);
+    mbar_init(&sh->drain, 1);
+    for (int i = 0; i < kMsgs; ++i) {
+      mbar_init(&sh->msg_full[i], 1);
+      mbar_init(&sh->msg_empty[i], 8 + 1 + 2);
+    }
+    sh->abort = 0;
+    sh->run = 0;
+    fence_barrier_init();
+  }
+  if (warp == 8) tmem_alloc(&sh->tmem, kTmemCols);
+  pdl_begin();
+  tc_fence_before();
+  find_run(a, sh);  // its barriers publish the above
+  tc_fence_after();
+  const uint32_t tiles = smem_u32(smem), tmem = sh->tmem;
+  // Of the 384 * 168 registers of the launch, 208 to each softmax thread (a row's
+  // 128 scores and their weights stay in registers), 88 to the others.
+  bool ok = true;
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int row = tid & 127, t = (int)a.by_group((uint32_t)row);
+    Softmax<T, DP> s{a, sh, tmem + ((uint32_t)(warp & 3) << 21), warp >> 2, row, t,
+                     row - t * a.group, 0, {0, 0}, 0};
+    ok = s.run();
+  } else if (warp == 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (elect_one()) {
+      Issuer<T, DP> s(a, sh, tiles, tmem);
+      ok = s.run();
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp < 11) {
+      Loader<DP, false> s(a, sh, tiles, tid - 9 * 32);
+      ok = s.run();
+      s.drain();
+    } else {
+      Loader<DP, true> s(a, sh, tiles, tid - 9 * 32);
+      ok = 
+    }
+  }
+  if (!ok) {
+    sh->abort = 1;
+    set_status(a.status, SPEC_ETIMEOUT);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  // After a wait that ran out nothing is combined from this CTA.
+  if (tid == 0 && sh->abort) a.rec[blockIdx.x] = AttendRec{};
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Joining the parts of divided units
+// ---------------------------------------------------------------------------
+constexpr int kCombineThreads = 128;
+constexpr int kCombineSplit = 16;  // blocks per unit
+template <typename T, int DP>
+__global__ void __launch_bounds__(kCombineThreads) attend_combine_kernel(const __grid_constant__ AttendArgs a) {
+  pdl_begin();
+  const int c = blockIdx.x;
+  const AttendRec rec = a.rec[c];
+  if (!rec.head) return;
+  int last = min(c + 1, a.ctas - 1);  // CTAs c .. last hold the unit's parts
+  while (last + 1 < a.ctas && a.rec[last].first && a.rec[last].first_cont) ++last;
+  const int tpt = a.shape.tpt;
+  const bool two = rec.ntok > tpt;
+  const int lane = threadIdx.x & 31;
+  constexpr int kCols = DP / 32;
+  for (int row = blockIdx.y * (kCombineThreads / 32) + (threadIdx.x >> 5);
+       row < (two ? 2 : 1) * kTileRows; row += kCombineSplit * (kCombineThreads / 32)) {
+    const int w = row / kTileRows, rt = (row % kTileRows) / a.group, g = row % kTileRows % a.group;
+    const int tok = w * tpt + rt;
+    if (rt >= tpt || tok >= rec.ntok) continue;
+    float m = -INFINITY;
+    for (int x = c; x <= last; ++x) {
+      const long long prow = (2LL * x + (x == c ? 1 : 0)) * 2 * kTileRows + row;
+      m = fmaxf(m, a.part_ml[prow].x);
+    }
+    float l = 0.0f, o[kCols];
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) o[i] = 0.0f;
+    for (int x = c; x <= last; ++x) {
+      const long long prow = (2LL * x + (x == c ? 1 : 0)) * 2 * kTileRows + row;
+      const float2 ml = a.part_ml[prow];
+      const float f = weight(ml.x, m);
+      l = fmaf(f, ml.y, l);
+      const float* src = a.part_o + prow * DP + lane * kCols;
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) o[i] = f == 0.0f ? o[i] : fmaf(f, src[i], o[i]);
+    }
+    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+    const int r = rec.row0 + rec.tok0 + tok, qh = rec.h * a.group + g;
+    if (lane * kCols < a.dim) {
+      uint32_t* dst = reinterpret_cast<uint32_t*>(
+          a.out + r * a.ld_out + ((long long)qh * a.dim + lane * kCols) * 2);
+#pragma unroll
+      for (int i = 0; i < kCols; i += 2) dst[i / 2] = Pack<T>::two(o[i] * inv, o[i + 1] * inv);
+    }
+    if (lane == 0 && a.lse)
+      a.lse[(long long)r * a.q_heads + qh] =
+          l > 0.0f || l != l ? (float)((m + log2f(l)) * kLn2) : -INFINITY;
+  }
+}
+
+template <typename T, int DP>
+cudaError_t launch(const AttendArgs& a, cudaStream_t st) {
+  const size_t smem = Tile<DP>::kSmemTiles + sizeof(Shared);
+  cudaError_t e = reserve_dyn_smem(attend_kernel<T, DP>, smem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(attend_kernel<T, DP>, dim3(a.ctas), dim3(kThreads), smem, st, a);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attend_combine_kernel<T, DP>, dim3(a.ctas, kCombineSplit),
+                    dim3(kCombineThreads), 0, st, a);
+}
+
+}  // namespace
+
+namespace {
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      p = nullptr;
+    }
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn;
+}
+}  // namespace
+
+// Query rows: (column, head of the group, K/V head, row), a box holds the
+// whole tokens of a tile in the order of the tile's rows. Packed K/V rows: (column,
+// head, row), boxes of 128 rows. Pages: (column, head, row, block), boxes of a
+// whole page where its rows divide the tile, or of 128 rows where the tile's
+// rows divide the page; a box begins on a whole 1024-byte swizzle atom, so
+// pages of fewer than 8 rows are left to the row copies. Boxes have 64 columns;
+// those past the head's end are filled with zeros.
+cudaError_t attend_maps(AttendArgs* a) {
+  const EncodeFn encode = encode_fn();
+  if (!encode) return cudaErrorNotSupported;
+  auto form = [&](CUtensorMap* map, const void* p, cuuint32_t rank, const cuuint64_t* dims,
+                  const cuuint64_t* strides, const cuuint32_t* box) {
+    const cuuint32_t step[4] = {1, 1, 1, 1};
+    return encode(map,
+                  a->dtype == SPEC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                  rank, const_cast<void*>(p), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  const cuuint64_t head = (cuuint64_t)a->dim * 2;
+  {
+    const cuuint64_t dims[4] = {(cuuint64_t)a->dim, (cuuint64_t)a->group, (cuuint64_t)a->kv_heads,
+                                (cuuint64_t)a->T};
+    const cuuint64_t strides[3] = {head, head * a->group, (cuuint64_t)a->ld_q};
+    const cuuint32_t box[4] = {64, (cuuint32_t)a->group, 1, (cuuint32_t)a->shape.tpt};
+    if (!form(&a->map_q, a->q, 4, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  const int bs = a->block_size;
+  a->box_rows = kTileKeys;
+  if (a->tables && bs % kTileKeys != 0) a->box_rows = (bs >= 8 && kTileKeys % bs == 0) ? bs : 0;
+  if (!a->box_rows) return cudaSuccess;
+  for (int v = 0; v < 2; ++v) {
+    const cuuint64_t dims[4] = {(cuuint64_t)a->dim, (cuuint64_t)a->kv_heads,
+                                (cuuint64_t)(a->tables ? bs : a->T), (cuuint64_t)a->num_blocks};
+    const cuuint64_t strides[3] = {head, (cuuint64_t)(v ? a->ld_v : a->ld_k),
+                                   (cuuint64_t)a->page_bytes};
+    const cuuint32_t box[4] = {64, 1, (cuuint32_t)a->box_rows, 1};
+    if (!form(v ? &a->map_v : &a->map_k, v ? a->v : a->k, a->tables ? 4 : 3, dims, strides, box))
+      return cudaErrorInvalidValue;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
+  if (a.dtype == SPEC_BF16)
+    return a.dim <= 64 ? launch<__nv_bfloat16, 64>(a, st) : launch<__nv_bfloat16, 128>(a, st);
+  return a.dim <= 64 ? launch<__half, 64>(a, st) : launch<__half, 128>(a, st);
+}
+
+}  // namespace specv
