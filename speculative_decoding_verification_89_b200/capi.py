@@ -101,13 +101,14 @@ class SpecError(RuntimeError):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    # What torch.cuda.current_stream().cuda_stream gives, without its 6 us in Python.
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _dtype_code(t):
@@ -303,15 +304,15 @@ def _kv_shapes(kv_stage, kv_pool, hid_stage, num_blocks, block_size):
 
 
 def _on_current_device(t):
-    if t.device.index != torch.cuda.current_device():
+    if not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
         raise ValueError(f"tensors are on {t.device}, not on the current device")
 
 
-def _int_tensor(t, dtype, shape, name, like):
-    """t must be a contiguous tensor of this type and shape on like's device."""
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or \
-            t.device != like.device:
-        raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on {like.device}")
+def _int_tensor(t, dtype, shape, name, device):
+    """t must be a contiguous tensor of this type and shape on the device (its index)."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or \
+            not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on cuda:{device}")
 
 
 def spec_extend_paged(block_tables, seq_lens, add_len, free_stack, free_top, new_lens, new_top,
@@ -322,43 +323,47 @@ def spec_extend_paged(block_tables, seq_lens, add_len, free_stack, free_top, new
     rows' pool slots into slot_map int64 [capacity]."""
     B, max_blocks = block_tables.shape
     _on_current_device(block_tables)
-    i32 = torch.int32
-    _int_tensor(block_tables, i32, (B, max_blocks), "block_tables", block_tables)
-    for name, t in (("seq_lens", seq_lens), ("add_len", add_len), ("new_lens", new_lens)):
-        _int_tensor(t, i32, (B,), name, block_tables)
-    for name, t in (("free_top", free_top), ("new_top", new_top), ("dev_status", dev_status)):
-        _int_tensor(t, i32, (1,), name, block_tables)
-    _int_tensor(free_stack, i32, (free_stack.numel(),), "free_stack", block_tables)
-    _int_tensor(row_off, i32, (B + 1,), "row_off", block_tables)
+    dev, i32, num_blocks = block_tables.get_device(), torch.int32, free_stack.numel()
+    _int_tensor(block_tables, i32, (B, max_blocks), "block_tables", dev)
+    _int_tensor(seq_lens, i32, (B,), "seq_lens", dev)
+    _int_tensor(add_len, i32, (B,), "add_len", dev)
+    _int_tensor(new_lens, i32, (B,), "new_lens", dev)
+    _int_tensor(free_top, i32, (1,), "free_top", dev)
+    _int_tensor(new_top, i32, (1,), "new_top", dev)
+    _int_tensor(dev_status, i32, (1,), "dev_status", dev)
+    _int_tensor(free_stack, i32, (num_blocks,), "free_stack", dev)
+    _int_tensor(row_off, i32, (B + 1,), "row_off", dev)
     capacity = 0
     if slot_map is not None:
         capacity = slot_map.numel()
-        _int_tensor(slot_map, torch.int64, (capacity,), "slot_map", block_tables)
+        _int_tensor(slot_map, torch.int64, (capacity,), "slot_map", dev)
     rc = _lib.spec_extend_paged(
         B, block_size, max_blocks, _ptr(block_tables), _ptr(seq_lens), _ptr(add_len),
-        _ptr(free_stack), _ptr(free_top), free_stack.numel(), _ptr(new_lens), _ptr(new_top),
+        _ptr(free_stack), _ptr(free_top), num_blocks, _ptr(new_lens), _ptr(new_top),
         _ptr(row_off), _ptr(slot_map), capacity, _ptr(dev_status), _stream(stream))
     _check("spec_extend_paged", rc)
 
 
 def _token_rows(t, shape, dtype, device, name):
     """Row stride (elements) of a [T, heads, head_dim] tensor whose rows are
-    contiguous."""
+    contiguous, on the device (its index)."""
     T, H, D = shape
-    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} must be {dtype} {list(shape)} on {device}")
-    if T * H * D and (t.stride(2) != 1 and D > 1 or t.stride(1) != D and H > 1):
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+        raise ValueError(f"{name} must be {dtype} {list(shape)} on cuda:{device}")
+    ld, sh, sd = t.stride()
+    if T * H * D and (sd != 1 and D > 1 or sh != D and H > 1):
         raise ValueError(f"each row of {name} must be contiguous")
-    return t.stride(0) if T > 1 else H * D
+    return ld if T > 1 else H * D
 
 
-def _pool_sizes(kv_pool, layer, like):
+def _pool_sizes(kv_pool, layer, dtype, device):
     """[num_blocks, layers, 2, block_size, kv_heads, head_dim] of a pool."""
-    if kv_pool.dim() != 6 or kv_pool.shape[2] != 2 or not kv_pool.is_contiguous() or \
-            kv_pool.dtype != like.dtype or kv_pool.device != like.device:
+    shape = kv_pool.shape
+    if len(shape) != 6 or shape[2] != 2 or kv_pool.dtype is not dtype or \
+            kv_pool.get_device() != device or not kv_pool.is_contiguous():
         raise ValueError("kv_pool must be contiguous [num_blocks, layers, 2, block_size, "
-                         f"kv_heads, head_dim], {like.dtype} on {like.device}")
-    N, layers, _, bs, H, D = kv_pool.shape
+                         f"kv_heads, head_dim], {dtype} on cuda:{device}")
+    N, layers, _, bs, H, D = shape
     if not 0 <= layer < layers:
         raise ValueError(f"layer {layer} outside the pool's {layers}")
     return N, layers, bs, H, D
@@ -371,11 +376,14 @@ def spec_store_kv(k, v, slot_map, kv_pool, layer, dev_status, stream=None):
     _on_current_device(k)
     if k.element_size() != 2:
         raise TypeError(f"K/V rows must have 2-byte elements, got {k.dtype}")
-    N, layers, bs, H, D = _pool_sizes(kv_pool, layer, k)
+    dev, dtype = k.get_device(), k.dtype
+    N, layers, bs, H, D = _pool_sizes(kv_pool, layer, dtype, dev)
     shape = (k.shape[0], H, D)
-    ld_k = _token_rows(k, shape, k.dtype, k.device, "k")
-    ld_v = _token_rows(v, shape, k.dtype, k.device, "v")
-    _int_tensor(slot_map, torch.int64, (shape[0],), "slot_map", k)
+    ld_k = _token_rows(k, shape, dtype, dev, "k")
+    ld_v = _token_rows(v, shape, dtype, dev, "v")
+    _int_tensor(slot_map, torch.int64, (shape[0],), "slot_map", dev)
+    if dev_status is not None:
+        _int_tensor(dev_status, torch.int32, (1,), "dev_status", dev)
     rc = _lib.spec_store_kv(_ptr(k), ld_k, _ptr(v), ld_v, shape[0], _ptr(slot_map),
                             _ptr(kv_pool), N, layers, layer, bs, H, D, _ptr(dev_status),
                             _stream(stream))
@@ -387,11 +395,12 @@ def spec_attend_workspace_bytes(head_dim):
 
 
 def attend_workspace(head_dim, device="cuda"):
-    """A workspace tensor of the size an attention call needs."""
+    """A zero-filled workspace tensor of the size an attention call needs; calls
+    leave it ready for the next one."""
     n = spec_attend_workspace_bytes(head_dim)
     if n == 0:
         raise ValueError("invalid sizes")
-    return torch.empty(n, dtype=torch.uint8, device=device)
+    return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
 def _attend_dtype(q):
@@ -402,21 +411,21 @@ def _attend_dtype(q):
     raise TypeError(f"attention takes bfloat16 or float16, got {q.dtype}")
 
 
-def _attend_common(q, out, lse, row_off, ws):
+def _attend_common(q, out, lse, row_off, dev_status, ws):
     _on_current_device(q)
-    code = _attend_dtype(q)
-    T, Hq, D = shape = tuple(q.shape)
-    ld_q = _token_rows(q, shape, q.dtype, q.device, "q")
-    ld_out = _token_rows(out, shape, q.dtype, q.device, "out")
+    code, dev = _attend_dtype(q), q.get_device()
+    T, Hq, D = shape = q.shape
+    ld_q = _token_rows(q, shape, q.dtype, dev, "q")
+    ld_out = _token_rows(out, shape, q.dtype, dev, "out")
     if lse is not None:
-        _int_tensor(lse, torch.float32, (T, Hq), "lse", q)
+        _int_tensor(lse, torch.float32, (T, Hq), "lse", dev)
     if row_off is not None:
-        _int_tensor(row_off, torch.int32, (row_off.numel(),), "row_off", q)
-        if row_off.numel() < 1:
-            raise ValueError("row_off must be int32 [B+1]")
-    if ws.device != q.device:
-        raise ValueError(f"the workspace must be on {q.device}")
-    return code, T, Hq, D, ld_q, ld_out
+        _int_tensor(row_off, torch.int32, (max(row_off.numel(), 1),), "row_off", dev)
+    if dev_status is not None:
+        _int_tensor(dev_status, torch.int32, (1,), "dev_status", dev)
+    if ws.get_device() != dev:
+        raise ValueError(f"the workspace must be on cuda:{dev}")
+    return code, dev, T, Hq, D, ld_q, ld_out
 
 
 def spec_attend_prompt(q, k, v, row_off, out, dev_status, ws, scale=None, lse=None, stream=None):
@@ -424,10 +433,10 @@ def spec_attend_prompt(q, k, v, row_off, out, dev_status, ws, scale=None, lse=No
     k, v [T, kv_heads, head_dim] (bfloat16 or float16, contiguous rows at any
     stride), row_off int32 [B+1]; scale defaults to head_dim ** -0.5; lse optional float32
     [T, q_heads]."""
-    code, T, Hq, D, ld_q, ld_out = _attend_common(q, out, lse, row_off, ws)
+    code, dev, T, Hq, D, ld_q, ld_out = _attend_common(q, out, lse, row_off, dev_status, ws)
     shape = (T, k.shape[1], D)
-    ld_k = _token_rows(k, shape, q.dtype, q.device, "k")
-    ld_v = _token_rows(v, shape, q.dtype, q.device, "v")
+    ld_k = _token_rows(k, shape, q.dtype, dev, "k")
+    ld_v = _token_rows(v, shape, q.dtype, dev, "v")
     rc = _lib.spec_attend_prompt(
         _ptr(q), ld_q, _ptr(k), ld_k, _ptr(v), ld_v, code, _ptr(row_off), row_off.numel() - 1, T,
         Hq, k.shape[1], D, D ** -0.5 if scale is None else scale, _ptr(out), ld_out, _ptr(lse),
@@ -442,13 +451,13 @@ def spec_attend_paged(q, kv_pool, layer, block_tables, seq_lens, out, dev_status
     same number of rows for each sequence; kv_pool as for spec_commit_paged;
     kv_stage [B, Kp1, layers, 2, kv_heads, head_dim] if the new rows' K/V are
     staged, None if seq_lens counts them already."""
-    code, T, Hq, D, ld_q, ld_out = _attend_common(q, out, lse, row_off, ws)
-    N, layers, bs, H, Dp = _pool_sizes(kv_pool, layer, q)
+    code, dev, T, Hq, D, ld_q, ld_out = _attend_common(q, out, lse, row_off, dev_status, ws)
+    N, layers, bs, H, Dp = _pool_sizes(kv_pool, layer, q.dtype, dev)
     if Dp != D:
         raise ValueError("q and kv_pool have different head sizes")
     B, max_blocks = block_tables.shape
-    _int_tensor(block_tables, torch.int32, (B, max_blocks), "block_tables", q)
-    _int_tensor(seq_lens, torch.int32, (B,), "seq_lens", q)
+    _int_tensor(block_tables, torch.int32, (B, max_blocks), "block_tables", dev)
+    _int_tensor(seq_lens, torch.int32, (B,), "seq_lens", dev)
     if row_off is not None and row_off.numel() != B + 1:
         raise ValueError("row_off must be int32 [B+1]")
     if row_off is None and B and T % B:
@@ -456,8 +465,8 @@ def spec_attend_paged(q, kv_pool, layer, block_tables, seq_lens, out, dev_status
     Kp1 = 0
     if kv_stage is not None:
         Kp1 = kv_stage.shape[1]
-        if tuple(kv_stage.shape) != (B, Kp1, layers, 2, H, D) or kv_stage.dtype != q.dtype or \
-                not kv_stage.is_contiguous() or kv_stage.device != q.device:
+        if kv_stage.shape != (B, Kp1, layers, 2, H, D) or kv_stage.dtype is not q.dtype or \
+                kv_stage.get_device() != dev or not kv_stage.is_contiguous():
             raise ValueError("kv_stage must be contiguous [B, Kp1, layers, 2, kv_heads, head_dim]")
     rc = _lib.spec_attend_paged(
         _ptr(q), ld_q, code, _ptr(row_off), T // B if B else 0, B, T, Hq, _ptr(kv_pool), N,

@@ -53,6 +53,7 @@ struct Msg {
   int c0, c1;        // tiles of each accumulator
   int two;           // two query tiles
   int part;          // 0 whole, 1 a later part of its unit, 2 the first of several
+  int head, parts;   // (parts) the CTA that has the first one, how many there are
   int end;           // no piece: the run is over
 };
 constexpr int kMsgs = 4;
@@ -62,12 +63,13 @@ struct Shared {
   uint64_t full[8], empty[8], landed[8];
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t o_empty, swap, drain;
+  uint64_t parted, ticketed;
   uint32_t tmem;
-  int abort;
   long long warp_sum[kThreads / 32];
   AttendSeq seq;      // the first unit's sequence
   int start[4];       // sequence, head, unit, cost taken of it
-  long long run;      // cost of this CTA's run
+  long long from, run, share;  // start and cost of this CTA's run, cost of a full one
+  int last;           // this CTA wrote the last part of a unit
   Msg msg[kMsgs];
   float2 ml[2][kTileRows];
 };
@@ -199,6 +201,8 @@ __device__ __forceinline__ void find_run(const AttendArgs& a, Shared* sh) {
         sh->start[2] = lo;
         sh->start[3] = (int)(lo ? y - shape.cost_before(s, lo) : y);
         sh->run = to - from;
+        sh->from = from;
+        sh->share = share;
         break;
       }
       at += head * a.kv_heads;
@@ -613,7 +617,6 @@ struct Loader {
   __device__ bool schedule() {
     Cursor cur_ = cursor(a, sh);
     MsgRing out, in;
-    AttendRec rec = {};
     int ahead = 0;
     bool over = false;
     for (;;) {
@@ -638,15 +641,12 @@ struct Loader {
             q->c0 = two ? first_tile_count(a.shape, x) : (m + 1) / 2;
             q->c1 = two ? m : m / 2;
             q->part = x.t0 > 0 ? 1 : x.t1 < x.nt ? 2 : 0;
-            if (x.t0 > 0) {
-              rec.first = 1;
-              rec.first_cont = x.t1 < x.nt;
-            } else if (x.t1 < x.nt) {
-              rec.head = 1;
-              rec.row0 = x.s.row0;
-              rec.tok0 = x.tok0;
-              rec.ntok = x.ntok;
-              rec.h = x.h;
+            if (q->part) {
+              // The unit's place on the cost line: a later part begins with the
+              // run, a first one ends with it.
+              const long long at = x.t0 > 0 ? sh->from - x.t0 : sh->from + sh->run - x.t1;
+              q->head = (int)quotient(at, sh->share);
+              q->parts = (int)quotient(at + x.nt - 1, sh->share) - q->head + 1;
             }
           }
           mbar_arrive(&sh->msg_full[out.i]);
@@ -662,7 +662,6 @@ struct Loader {
       begin();
       if (!fill()) return false;
     }
-    if (lane == 0) a.rec[blockIdx.x] = rec;
     return true;
   }
 };
@@ -807,7 +806,7 @@ struct Softmax {
   uint32_t tmem;    // with this warp's lanes
   int w, row;       // warpgroup, row of the tile
   int tok, head;    // row's token within a tile and query head within the group
-  uint32_t s_ph, o_ph[2], x_ph;
+  uint32_t s_ph, o_ph[2], x_ph, part_ph;
 
   __device__ bool wait(uint64_t* bar, uint32_t ph) {
     return __all_sync(0xffffffffu, wait_bar(bar, ph));
@@ -1000,10 +999,10 @@ struct Softmax {
           read_o(c, has0, f0, has1, f1, o);
           if (valid && whole) write_out(dst, c, o);
           if (valid && !whole) {
-            float4* po = reinterpret_cast<float4*>(a.part_o + prow * DP + c);
+            float4* po = part_o(slot, two ? w : 0, c / 4);
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
-              po[i / 4] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+              po[(i / 4) * kTileRows + row] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           }
         }
         if (valid && (two || w == 0)) {
@@ -1021,6 +1020,105 @@ struct Softmax {
         o_ph[w ^ 1] ^= 1;
       }
       if (p.m > 0) arrive(&sh->o_empty);
+      if (!whole && !join_parts(p)) return false;
+    }
+  }
+  // Columns [4 * c4, ...) of a part's tile: four columns of all rows, then the next four.
+  __device__ __forceinline__ float4* part_o(long long slot, int tile, int c4) const {
+    return reinterpret_cast<float4*>(a.part_o) +
+           ((slot * 2 + tile) * (DP / 4) + c4) * kTileRows;
+  }
+  // A part of a divided unit is written: the CTA that counts the unit's last one
+  // joins them, in their order, and leaves the count at zero.
+  __device__ bool join_parts(const Msg& p) {
+    __threadfence();
+    arrive(&sh->parted);
+    if (threadIdx.x < 32) {
+      if (!wait(&sh->parted, part_ph)) return false;
+      if (threadIdx.x == 0) {
+        int n;
+        asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
+                     : "=r"(n)
+                     : "l"(a.counts + p.head)
+                     : "memory");
+        sh->last = n == p.parts - 1;
+        if (sh->last) a.counts[p.head] = 0;
+        mbar_arrive(&sh->ticketed);
+      }
+      __syncwarp();
+    }
+    if (!wait(&sh->ticketed, part_ph)) return false;
+    part_ph ^= 1;
+    if (!sh->last) return true;
+    fence_acq_rel();
+    const int tpt = a.shape.tpt;
+#pragma unroll 1
+    for (int t = 0; t <= p.two; ++t) {
+      const int rows = min(tpt, p.ntok - t * tpt) * a.group;
+      // Reads of several rows or of several parts at once: each takes about 700 cycles.
+      if (rows * (DP / 4) > 512) join_rows<8, 1>(p, t, rows);
+      else join_rows<1, 8>(p, t, rows);
+    }
+    return true;
+  }
+  template <int kItems, int kParts>
+  __device__ __forceinline__ void join_rows(const Msg& p, int t, int rows) {
+    const int items = rows * (DP / 4);
+#pragma unroll 1
+    for (int i0 = threadIdx.x; i0 < items; i0 += 256 * kItems) {
+      float m[kItems], l[kItems], o[kItems][4];
+      int c4[kItems], r[kItems];
+#pragma unroll
+      for (int u = 0; u < kItems; ++u) {
+        const int i = min(i0 + 256 * u, items - 1);
+        c4[u] = i / rows;
+        r[u] = i - c4[u] * rows;
+        m[u] = -INFINITY;
+        l[u] = o[u][0] = o[u][1] = o[u][2] = o[u][3] = 0.0f;
+      }
+#pragma unroll 1
+      for (int k0 = 0; k0 < p.parts; k0 += kParts) {
+        float2 ml[kParts][kItems];
+        float4 v[kParts][kItems];
+#pragma unroll
+        for (int k = 0; k < kParts; ++k)
+#pragma unroll
+          for (int u = 0; u < kItems; ++u) {
+            const int part = min(k0 + k, p.parts - 1);
+            const long long slot = 2 * (p.head + part) + (part == 0 ? 1 : 0);
+            ml[k][u] = __ldcg(a.part_ml + (slot * 2 + t) * kTileRows + r[u]);
+            v[k][u] = __ldcg(part_o(slot, t, c4[u]) + r[u]);
+          }
+#pragma unroll
+        for (int k = 0; k < kParts; ++k)
+#pragma unroll
+          for (int u = 0; u < kItems; ++u) {
+            if (k0 + k >= p.parts) continue;
+            const float top = fmaxf(m[u], ml[k][u].x);
+            const float f = weight(m[u], top), g = weight(ml[k][u].x, top);
+            l[u] = f * l[u] + g * ml[k][u].y;
+            o[u][0] = f * o[u][0] + (g == 0.0f ? 0.0f : g * v[k][u].x);
+            o[u][1] = f * o[u][1] + (g == 0.0f ? 0.0f : g * v[k][u].y);
+            o[u][2] = f * o[u][2] + (g == 0.0f ? 0.0f : g * v[k][u].z);
+            o[u][3] = f * o[u][3] + (g == 0.0f ? 0.0f : g * v[k][u].w);
+            m[u] = top;
+          }
+      }
+#pragma unroll
+      for (int u = 0; u < kItems; ++u) {
+        if (i0 + 256 * u >= items) continue;
+        const bool some = l[u] > 0.0f || l[u] != l[u];
+        const float inv = some ? __fdividef(1.0f, l[u]) : 0.0f;
+        const int tk = (int)a.by_group((uint32_t)r[u]), qh = p.h * a.group + r[u] - tk * a.group;
+        const long long token = p.s.row0 + p.tok0 + t * a.shape.tpt + tk;
+        if (c4[u] * 4 < a.dim)
+          *reinterpret_cast<uint2*>(a.out + token * a.ld_out +
+                                    ((long long)qh * a.dim + c4[u] * 4) * 2) =
+              make_uint2(Pack<T>::two(o[u][0] * inv, o[u][1] * inv),
+                         Pack<T>::two(o[u][2] * inv, o[u][3] * inv));
+        if (c4[u] == 0 && a.lse)
+          a.lse[token * a.q_heads + qh] = some ? (m[u] + __log2f(l[u])) * (float)kLn2 : -INFINITY;
+      }
     }
   }
 };
@@ -1044,11 +1142,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     mbar_init(&sh->o_empty, 8);
     mbar_init(&sh->swap, 8);
     mbar_init(&sh->drain, 1);
+    mbar_init(&sh->parted, 8);
+    mbar_init(&sh->ticketed, 1);
     for (int i = 0; i < kMsgs; ++i) {
       mbar_init(&sh->msg_full[i], 1);
       mbar_init(&sh->msg_empty[i], 8 + 1 + 2);
     }
-    sh->abort = 0;
     sh->run = 0;
     fence_barrier_init();
   }
@@ -1065,7 +1164,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int row = tid & 127, t = (int)a.by_group((uint32_t)row);
     Softmax<T, DP> s{a, sh, tmem + ((uint32_t)(warp & 3) << 21), warp >> 2, row, t,
-                     row - t * a.group, 0, {0, 0}, 0};
+                     row - t * a.group, 0, {0, 0}, 0, 0};
     ok = s.run();
   } else if (warp == 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
@@ -1084,71 +1183,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       ok = s.schedule();
     }
   }
-  if (!ok) {
-    sh->abort = 1;
-    set_status(a.status, SPEC_ETIMEOUT);
-  }
+  if (!ok) set_status(a.status, SPEC_ETIMEOUT);
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  // After a wait that ran out nothing is combined from this CTA.
-  if (tid == 0 && sh->abort) a.rec[blockIdx.x] = AttendRec{};
   if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
-  }
-}
-
-// ---------------------------------------------------------------------------
-// Joining the parts of divided units
-// ---------------------------------------------------------------------------
-constexpr int kCombineThreads = 128;
-constexpr int kCombineSplit = 16;  // blocks per unit
-template <typename T, int DP>
-__global__ void __launch_bounds__(kCombineThreads) attend_combine_kernel(const __grid_constant__ AttendArgs a) {
-  pdl_begin();
-  const int c = blockIdx.x;
-  const AttendRec rec = a.rec[c];
-  if (!rec.head) return;
-  int last = min(c + 1, a.ctas - 1);  // CTAs c .. last hold the unit's parts
-  while (last + 1 < a.ctas && a.rec[last].first && a.rec[last].first_cont) ++last;
-  const int tpt = a.shape.tpt;
-  const bool two = rec.ntok > tpt;
-  const int lane = threadIdx.x & 31;
-  constexpr int kCols = DP / 32;
-  for (int row = blockIdx.y * (kCombineThreads / 32) + (threadIdx.x >> 5);
-       row < (two ? 2 : 1) * kTileRows; row += kCombineSplit * (kCombineThreads / 32)) {
-    const int w = row / kTileRows, rt = (row % kTileRows) / a.group, g = row % kTileRows % a.group;
-    const int tok = w * tpt + rt;
-    if (rt >= tpt || tok >= rec.ntok) continue;
-    float m = -INFINITY;
-    for (int x = c; x <= last; ++x) {
-      const long long prow = (2LL * x + (x == c ? 1 : 0)) * 2 * kTileRows + row;
-      m = fmaxf(m, a.part_ml[prow].x);
-    }
-    float l = 0.0f, o[kCols];
-#pragma unroll
-    for (int i = 0; i < kCols; ++i) o[i] = 0.0f;
-    for (int x = c; x <= last; ++x) {
-      const long long prow = (2LL * x + (x == c ? 1 : 0)) * 2 * kTileRows + row;
-      const float2 ml = a.part_ml[prow];
-      const float f = weight(ml.x, m);
-      l = fmaf(f, ml.y, l);
-      const float* src = a.part_o + prow * DP + lane * kCols;
-#pragma unroll
-      for (int i = 0; i < kCols; ++i) o[i] = f == 0.0f ? o[i] : fmaf(f, src[i], o[i]);
-    }
-    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-    const int r = rec.row0 + rec.tok0 + tok, qh = rec.h * a.group + g;
-    if (lane * kCols < a.dim) {
-      uint32_t* dst = reinterpret_cast<uint32_t*>(
-          a.out + r * a.ld_out + ((long long)qh * a.dim + lane * kCols) * 2);
-#pragma unroll
-      for (int i = 0; i < kCols; i += 2) dst[i / 2] = Pack<T>::two(o[i] * inv, o[i + 1] * inv);
-    }
-    if (lane == 0 && a.lse)
-      a.lse[(long long)r * a.q_heads + qh] =
-          l > 0.0f || l != l ? (float)((m + log2f(l)) * kLn2) : -INFINITY;
   }
 }
 
@@ -1157,10 +1198,7 @@ cudaError_t launch(const AttendArgs& a, cudaStream_t st) {
   const size_t smem = Tile<DP>::kSmemTiles + sizeof(Shared);
   cudaError_t e = reserve_dyn_smem(attend_kernel<T, DP>, smem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(attend_kernel<T, DP>, dim3(a.ctas), dim3(kThreads), smem, st, a);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(attend_combine_kernel<T, DP>, dim3(a.ctas, kCombineSplit),
-                    dim3(kCombineThreads), 0, st, a);
+  return launch_pdl(attend_kernel<T, DP>, dim3(a.ctas), dim3(kThreads), smem, st, a);
 }
 
 }  // namespace

@@ -11,15 +11,6 @@ constexpr int kAttendMaxCtas = 148;
 constexpr int kAttendMaxGroup = kTileRows;  // query heads that share a K/V head
 constexpr int kAttendMaxDim = 128;
 
-// What a CTA leaves for the combine launch: whether its run begins inside a
-// unit (slot 2c holds that part) and, if so, whether the unit goes on past the
-// run; whether its last unit begins here and goes on (slot 2c + 1), and which
-// rows that unit has.
-struct AttendRec {
-  int first, first_cont, head;
-  int row0, tok0, ntok, h, pad;
-};
-
 struct AttendArgs {
   int B, T, q_heads, kv_heads, group, dim;
   int dtype;          // SPEC_BF16 or SPEC_F16
@@ -47,9 +38,9 @@ struct AttendArgs {
   long long stage_seq, stage_row;  // bytes between sequences, rows
   int stage_rows;
   int32_t* status;
-  float* part_o;     // [2 * ctas][2 * kTileRows][DP] unnormalised
+  float* part_o;     // [2 * ctas][2][DP / 4][kTileRows][4] unnormalised
   float2* part_ml;   // [2 * ctas][2 * kTileRows] (maximum in log2 units, sum)
-  AttendRec* rec;    // [ctas]
+  int32_t* counts;   // [ctas] parts written of the unit that CTA begins; 0 between calls
   int ctas;
   bool out_sectors;   // rows of heads in out begin on 32-byte boundaries
   // Tensors for tiled copies of 64 columns; those of K and V have box_rows rows,
@@ -61,7 +52,7 @@ struct AttendArgs {
 cudaError_t attend_maps(AttendArgs* a);
 // Workspace bytes of the parts, for rows padded to DP columns.
 struct AttendWs {
-  size_t o, ml, rec, total;
+  size_t o, ml, counts, total;
 };
 inline int attend_padded_dim(int dim) { return dim <= 64 ? 64 : 128; }
 inline AttendWs attend_ws(int dim) {
@@ -69,8 +60,8 @@ inline AttendWs attend_ws(int dim) {
   AttendWs w;
   w.o = 0;
   w.ml = rows * attend_padded_dim(dim) * sizeof(float);
-  w.rec = w.ml + rows * sizeof(float2);
-  w.total = (w.rec + kAttendMaxCtas * sizeof(AttendRec) + 255) & ~(size_t)255;
+  w.counts = w.ml + rows * sizeof(float2);
+  w.total = (w.counts + kAttendMaxCtas * sizeof(int32_t) + 255) & ~(size_t)255;
   return w;
 }
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st);

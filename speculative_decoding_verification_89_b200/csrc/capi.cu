@@ -176,7 +176,7 @@ int attend_args(const void* q, int64_t ld_q, int dtype, const int32_t* row_off, 
   a->status = dev_status;
   a->part_o = reinterpret_cast<float*>((char*)ws + w.o);
   a->part_ml = reinterpret_cast<float2*>((char*)ws + w.ml);
-  a->rec = reinterpret_cast<AttendRec*>((char*)ws + w.rec);
+  a->counts = reinterpret_cast<int32_t*>((char*)ws + w.counts);
   a->ctas = std::min(sm_count(), kAttendMaxCtas);
   return SPEC_OK;
 }

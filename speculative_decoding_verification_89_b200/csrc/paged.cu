@@ -48,24 +48,15 @@ __device__ longlong2 block_excl_scan2(longlong2 v, longlong2* tot) {
   return make_longlong2(base.x + incl.x - v.x, base.y + incl.y - v.y);
 }
 
-// One CTA checks everything, then takes the missing blocks off the stack
-// (sequences ascending, entries ascending) and writes lengths and offsets. The
-// order of the pops couples all sequences, hence the single CTA.
-__global__ void __launch_bounds__(kExtendThreads) extend_plan_kernel(ExtendArgs a) {
-  pdl_begin();
-  __shared__ int s_code, s_bad, s_st0;
-  if (threadIdx.x == 0) {
-    s_st0 = *(volatile int32_t*)a.status;
-    s_bad = 0;
-    s_code = SPEC_OK;
-  }
-  __syncthreads();
-  if (s_st0 != SPEC_OK) return;
+// What both forms of the call check, by the whole block: lengths and counts,
+// the entry of a part-filled last block, the stack. Sequences are dealt to threads
+// in runs of consecutive ones (their order is that of the pops); on return
+// cnt holds the thread's missing blocks and new rows, pre those of the sequences
+// before, tot all. SPEC_OK, or the code of the failure, the same in all threads.
+__device__ int extend_check(const ExtendArgs& a, int b0, int b1, int ft, longlong2* pre,
+                            longlong2* tot) {
   const int bs = a.block_size;
-  const int per = (a.B + blockDim.x - 1) / blockDim.x;
-  const int b0 = min(a.B, (int)threadIdx.x * per), b1 = min(a.B, b0 + per);
-  const int ft = *a.free_top;
-  longlong2 cnt = make_longlong2(0, 0);  // missing blocks, new rows
+  longlong2 cnt = make_longlong2(0, 0);
   int bad = 0;
   for (int b = b0; b < b1; ++b) {
     const int len = a.seq_lens[b], add = a.add_len[b];
@@ -82,29 +73,120 @@ __global__ void __launch_bounds__(kExtendThreads) extend_plan_kernel(ExtendArgs 
     cnt.x += blocks_for((long long)len + add, bs) - held;
     cnt.y += add;
   }
-  if (bad) s_bad = 1;
-  longlong2 tot;
-  const longlong2 pre = block_excl_scan2(cnt, &tot);  // its barriers publish s_bad
-  if (threadIdx.x == 0) {
-    if (s_bad || ft < 0 || ft > a.num_blocks || tot.y > INT32_MAX ||
-        (a.slot_map && tot.y > a.cap))
-      s_code = SPEC_EINVAL;
-    else if (tot.x > ft)
-      s_code = SPEC_ENOBLOCKS;
+  *pre = block_excl_scan2(cnt, tot);
+  if (__syncthreads_or(bad) || ft < 0 || ft > a.num_blocks || tot->y > INT32_MAX ||
+      (a.slot_map && tot->y > a.cap))
+    return SPEC_EINVAL;
+  if (tot->x > ft) return SPEC_ENOBLOCKS;
+  bad = 0;  // popped ids must be valid
+  for (int p = ft - (int)tot->x + threadIdx.x; p < ft; p += blockDim.x) {
+    const int id = a.free_stack[p];
+    if (id < 0 || id >= a.num_blocks) bad = 1;
   }
-  __syncthreads();
-  if (s_code == SPEC_OK) {  // popped ids must be valid
-    bad = 0;
-    for (int p = ft - (int)tot.x + threadIdx.x; p < ft; p += blockDim.x) {
-      const int id = a.free_stack[p];
-      if (id < 0 || id >= a.num_blocks) bad = 1;
+  return __syncthreads_or(bad) ? SPEC_EINVAL : SPEC_OK;
+}
+
+// One launch, a cluster of CTAs. Every CTA checks everything for itself and keeps
+// in shared memory, per sequence, its length and the rows, blocks to be popped and
+// blocks with new rows before it; once all have read the state (cluster
+// barrier), the blocks that hold new rows are dealt out, 16 lanes each: a
+// block's number comes from the table (a part-filled last block) or directly
+// from the stack, so nothing waits for a table entry.
+__global__ void __launch_bounds__(kExtendThreads) extend_kernel(ExtendArgs a) {
+  pdl_begin();
+  extern __shared__ int s_seq[];  // [4][B + 1]
+  int* s_len = s_seq;
+  int* s_row = s_len + a.B + 1;
+  int* s_pop = s_row + a.B + 1;
+  int* s_blk = s_pop + a.B + 1;
+  __shared__ int s_st0;
+  if (threadIdx.x == 0) s_st0 = *(volatile int32_t*)a.status;
+  const int bs = a.block_size, ft = *a.free_top;
+  const int per = (a.B + blockDim.x - 1) / blockDim.x;
+  const int b0 = min(a.B, (int)threadIdx.x * per), b1 = min(a.B, b0 + per);
+  longlong2 pre, tot;
+  const int code = extend_check(a, b0, b1, ft, &pre, &tot);  // its barriers publish s_st0
+  const bool run = s_st0 == SPEC_OK && code == SPEC_OK;      // the same in every CTA
+  long long nblk = 0;
+  if (run) {
+    longlong2 cnt = make_longlong2(0, 0), all;
+    for (int b = b0; b < b1; ++b) {
+      const int len = a.seq_lens[b], add = a.add_len[b];
+      if (add > 0) cnt.x += (len + add - 1) / bs - len / bs + 1;
     }
-    bad = __syncthreads_or(bad);
-    if (bad && threadIdx.x == 0) s_code = SPEC_EINVAL;
+    const longlong2 before = block_excl_scan2(cnt, &all);
+    nblk = all.x;
+    int row = (int)pre.y, pop = (int)pre.x, blk = (int)before.x;
+    for (int b = b0; b < b1; ++b) {
+      const int len = a.seq_lens[b], add = a.add_len[b];
+      s_len[b] = len;
+      s_row[b] = row;
+      s_pop[b] = pop;
+      s_blk[b] = blk;
+      row += add;
+      pop += (int)(blocks_for((long long)len + add, bs) - blocks_for(len, bs));
+      if (add > 0) blk += (len + add - 1) / bs - len / bs + 1;
+    }
+    if (threadIdx.x == 0) s_row[a.B] = (int)tot.y;
   }
+  // Every CTA has read lengths and stack height: new_lens and new_top may be theirs.
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (!run) {
+    if (blockIdx.x == 0 && threadIdx.x == 0 && s_st0 == SPEC_OK) set_status(a.status, code);
+    return;
+  }
+  if (blockIdx.x == 0) {
+    for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
+      a.row_off[b] = s_row[b];
+      a.new_lens[b] = s_len[b] + s_row[b + 1] - s_row[b];
+    }
+    if (threadIdx.x == 0) {
+      a.row_off[a.B] = (int)tot.y;
+      *a.new_top = ft - (int)tot.x;
+    }
+  }
+  const int lane = threadIdx.x & 15;
+  const int groups = gridDim.x * (blockDim.x / 16);
+  for (long long u = blockIdx.x * (blockDim.x / 16) + (threadIdx.x >> 4); u < nblk; u += groups) {
+    int lo = 0, hi = a.B - 1;  // the last sequence b with s_blk[b] <= u
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_blk[mid] <= u) lo = mid; else hi = mid - 1;
+    }
+    const int len = s_len[lo], add = s_row[lo + 1] - s_row[lo];
+    const int held = (int)blocks_for(len, bs), i = len / bs + (int)(u - s_blk[lo]);
+    int32_t* entry = a.tables + (size_t)lo * a.max_blocks + i;
+    const int id = i < held ? *entry : a.free_stack[ft - 1 - (s_pop[lo] + i - held)];
+    if (i >= held && lane == 0) *entry = id;
+    if (!a.slot_map) continue;
+    const int first = max(len, i * bs), end = (int)min((long long)len + add, (i + 1LL) * bs);
+    for (int pos = first + lane; pos < end; pos += 16)
+      a.slot_map[s_row[lo] + pos - len] = (long long)id * bs + pos - i * bs;
+  }
+  if (a.slot_map)
+    for (long long r = tot.y + (long long)blockIdx.x * blockDim.x + threadIdx.x; r < a.cap;
+         r += (long long)gridDim.x * blockDim.x)
+      a.slot_map[r] = -1;
+}
+
+// The plan of many rows or sequences: one CTA checks everything, then takes the
+// missing blocks off the stack (sequences ascending, entries ascending) and writes
+// lengths and offsets.
+__global__ void __launch_bounds__(kExtendThreads) extend_plan_kernel(ExtendArgs a) {
+  pdl_begin();
+  __shared__ int s_st0;
+  if (threadIdx.x == 0) s_st0 = *(volatile int32_t*)a.status;
   __syncthreads();
-  if (s_code != SPEC_OK) {
-    if (threadIdx.x == 0) set_status(a.status, s_code);
+  if (s_st0 != SPEC_OK) return;
+  const int bs = a.block_size;
+  const int per = (a.B + blockDim.x - 1) / blockDim.x;
+  const int b0 = min(a.B, (int)threadIdx.x * per), b1 = min(a.B, b0 + per);
+  const int ft = *a.free_top;
+  longlong2 pre, tot;
+  const int code = extend_check(a, b0, b1, ft, &pre, &tot);
+  if (code != SPEC_OK) {
+    if (threadIdx.x == 0) set_status(a.status, code);
     return;
   }
   int k = (int)pre.x, off = (int)pre.y;
@@ -145,32 +227,74 @@ __global__ void __launch_bounds__(kFillThreads) extend_fill_kernel(ExtendArgs a)
   }
 }
 
-// K and V rows to their slots: a warp per row, 16 bytes per lane and access.
+// K and V rows to their slots: a warp per token, up to four 16-byte vectors of
+// each row per lane in flight before the first is stored, loaded while the slot
+// is looked up. Bound by HBM (each byte read and written once): rows of 8 heads of
+// 128, 20000 tokens.
 constexpr int kStoreThreads = 256;
 __global__ void __launch_bounds__(kStoreThreads) store_kv_kernel(StoreArgs a) {
   pdl_begin();
   const int lane = threadIdx.x & 31;
-  const long long item = (long long)blockIdx.x * (kStoreThreads / 32) + (threadIdx.x >> 5);
-  if (item >= 2LL * a.T) return;
-  if (a.status && *(volatile int32_t*)a.status != SPEC_OK) return;
-  const int t = (int)(item >> 1), part = (int)(item & 1);
+  const int t = blockIdx.x * (kStoreThreads / 32) + (threadIdx.x >> 5);
+  if (t >= a.T) return;
+  const int st0 = a.status ? *(volatile int32_t*)a.status : SPEC_OK;
   const long long slot = a.slot_map[t];
-  if (slot == -1) return;
-  if (slot < -1 || slot >= (long long)a.num_blocks * a.block_size) {
+  const uint4* k = reinterpret_cast<const uint4*>(a.k + t * a.ld_k);
+  const uint4* v = reinterpret_cast<const uint4*>(a.v + t * a.ld_v);
+  const int n = a.row_bytes / 16;
+  uint4 x[4], y[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if (lane + 32 * u < n) {
+      x[u] = __ldcs(k + lane + 32 * u);
+      y[u] = __ldcs(v + lane + 32 * u);
+    }
+  if (st0 != SPEC_OK || slot == -1) return;
+  const long long slots = (long long)a.num_blocks * a.block_size;
+  if (slot < -1 || slot >= slots) {
     if (lane == 0) set_status(a.status, SPEC_EINVAL);
     return;
   }
-  const long long block = slot / a.block_size;
-  const int row = (int)(slot - block * a.block_size);
-  const uint4* src = reinterpret_cast<const uint4*>(part ? a.v + t * a.ld_v : a.k + t * a.ld_k);
+  const long long block =
+      slots <= INT32_MAX ? (uint32_t)slot / (uint32_t)a.block_size : slot / a.block_size;
   uint4* dst = reinterpret_cast<uint4*>(a.pool + block * a.page_bytes +
-                                        ((long long)part * a.block_size + row) * a.row_bytes);
-  for (int i = lane; i < a.row_bytes / 16; i += 32) dst[i] = __ldcs(src + i);
+                                        (slot - block * a.block_size) * a.row_bytes);
+  const long long to_v = (long long)a.block_size * n;  // V rows follow a block's K rows
+  for (int i = lane;;) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i + 32 * u < n) {
+        dst[i + 32 * u] = x[u];
+        dst[to_v + i + 32 * u] = y[u];
+      }
+    i += 128;
+    if (i - lane >= n) break;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i + 32 * u < n) {
+        x[u] = __ldcs(k + i + 32 * u);
+        y[u] = __ldcs(v + i + 32 * u);
+      }
+  }
 }
 
 }  // namespace
 
+// One launch where a cluster's CTAs do the writing in a few microseconds: up to
+// kClusterRows rows of slot map, by 8 CTAs (one for up to kOneCtaRows), and
+// sequences whose records fit its shared memory. Else a plan and a grid that fills
+// the map at the rate of the memory.
+constexpr long long kClusterRows = 1 << 20, kOneCtaRows = 8192;
+constexpr int kClusterSeqs = 8192;
+
 cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t st) {
+  if (a.B <= kClusterSeqs && a.cap <= kClusterRows) {
+    const size_t smem = 4 * ((size_t)a.B + 1) * sizeof(int);
+    const cudaError_t e = reserve_dyn_smem(extend_kernel, smem);
+    if (e != cudaSuccess) return e;
+    const unsigned ctas = a.cap <= kOneCtaRows ? 1 : 8;
+    return launch_pdl_cluster(extend_kernel, dim3(ctas), dim3(kExtendThreads), smem, st, ctas, a);
+  }
   cudaError_t e = launch_pdl(extend_plan_kernel, dim3(1), dim3(kExtendThreads), 0, st, a);
   if (e != cudaSuccess || !a.slot_map || a.cap == 0) return e;
   const long long want = (a.cap + kFillThreads - 1) / kFillThreads;
@@ -179,8 +303,7 @@ cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_store_kv(const StoreArgs& a, cudaStream_t st) {
-  const long long items = 2LL * a.T;
-  const unsigned grid = (unsigned)((items + kStoreThreads / 32 - 1) / (kStoreThreads / 32));
+  const unsigned grid = (unsigned)((a.T + (long long)kStoreThreads / 32 - 1) / (kStoreThreads / 32));
   return launch_pdl(store_kv_kernel, dim3(grid), dim3(kStoreThreads), 0, st, a);
 }
 

@@ -85,6 +85,19 @@ def test_extend_matches_the_oracle(B, bs, lo, hi, most, inplace):
                             int(got["top"]), bs, need + 2) == []
 
 
+@pytest.mark.parametrize("B,bs,most", [(3, 16, 400000), (9000, 16, 60), (8193, 1, 2),
+                                       (500, 64, 2100), (8192, 16, 127)])
+def test_extend_large(B, bs, most):
+    """Around the limits between one launch and two."""
+    rng = np.random.default_rng(B)
+    ctx, add = rng.integers(0, 100, B), rng.integers(0, most + 1, B)
+    need = int((-(-(ctx + add) // bs)).sum())
+    state = shuffled_state(ctx.tolist(), bs, int((-(-(ctx + add) // bs)).max()), need, B)
+    cap = int(add.sum()) + 5
+    got = run_extend(state, add.tolist(), cap, inplace=True)
+    same_extend(got, oracle_extend(state, add, cap), cap)
+
+
 def test_extend_without_a_map_and_by_nothing():
     state = shuffled_state([5, 0, 16], 16, 3, 8, 1)
     got = run_extend(state, [0, 0, 0], 0)
@@ -145,6 +158,7 @@ def test_extend_does_nothing_while_an_error_is_pending():
     (1, 1, 8, 1, 1, 0, torch.bfloat16), (9, 8, 128, 16, 2, 1, torch.bfloat16),
     (200, 2, 64, 16, 3, 2, torch.float16), (77, 3, 40, 24, 1, 0, torch.float16),
     (1000, 1, 128, 8, 2, 0, torch.bfloat16), (5, 16, 256, 16, 2, 1, torch.bfloat16),
+    (3, 9, 136, 4, 1, 0, torch.float16),
 ])
 def test_store_moves_rows_and_nothing_else(T, H, D, bs, layers, layer, dtype):
     capi = _capi()
