@@ -914,6 +914,7 @@ int spec_extend_paged(int B, int block_size, int max_blocks, int32_t* block_tabl
   ExtendArgs a;
   a.B = B;
   a.block_size = block_size;
+  a.by_bs = fast_div((uint32_t)block_size);
   a.max_blocks = max_blocks;
   a.num_blocks = num_blocks;
   a.tables = block_tables;

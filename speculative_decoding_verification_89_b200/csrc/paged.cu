@@ -14,7 +14,14 @@ namespace {
 constexpr int kExtendThreads = 1024;
 constexpr int kFillThreads = 256;
 
-__device__ __forceinline__ long long blocks_for(long long n, int bs) { return (n + bs - 1) / bs; }
+// Blocks of n <= 2^30 rows (64-bit divisions bound the one-launch form when it used
+// them: 28 us for 64 prompts of up to 4096 rows).
+__device__ __forceinline__ int blocks_for(const ExtendArgs& a, int n) {
+  return (int)a.by_bs((uint32_t)(n + a.block_size - 1));
+}
+__device__ __forceinline__ int block_of(const ExtendArgs& a, int pos) {
+  return (int)a.by_bs((uint32_t)pos);
+}
 
 // Block-wide exclusive scan of two counts per thread; totals in tot.
 __device__ longlong2 block_excl_scan2(longlong2 v, longlong2* tot) {
@@ -60,17 +67,16 @@ __device__ int extend_check(const ExtendArgs& a, int b0, int b1, int ft, longlon
   int bad = 0;
   for (int b = b0; b < b1; ++b) {
     const int len = a.seq_lens[b], add = a.add_len[b];
-    if (len < 0 || add < 0 || blocks_for((long long)len + add, bs) > a.max_blocks ||
-        (long long)len + add > INT32_MAX) {
+    if (len < 0 || add < 0 || (long long)len + add > (long long)a.max_blocks * bs) {
       bad = 1;
       continue;
     }
-    const int held = (int)blocks_for(len, bs);
+    const int held = blocks_for(a, len);
     if (add > 0 && held * (long long)bs > len) {  // rows go into the held last block
       const int id = a.tables[(size_t)b * a.max_blocks + held - 1];
       if (id < 0 || id >= a.num_blocks) bad = 1;
     }
-    cnt.x += blocks_for((long long)len + add, bs) - held;
+    cnt.x += blocks_for(a, len + add) - held;
     cnt.y += add;
   }
   *pre = block_excl_scan2(cnt, tot);
@@ -112,7 +118,7 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(ExtendArgs a) {
     longlong2 cnt = make_longlong2(0, 0), all;
     for (int b = b0; b < b1; ++b) {
       const int len = a.seq_lens[b], add = a.add_len[b];
-      if (add > 0) cnt.x += (len + add - 1) / bs - len / bs + 1;
+      if (add > 0) cnt.x += block_of(a, len + add - 1) - block_of(a, len) + 1;
     }
     const longlong2 before = block_excl_scan2(cnt, &all);
     nblk = all.x;
@@ -124,8 +130,8 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(ExtendArgs a) {
       s_pop[b] = pop;
       s_blk[b] = blk;
       row += add;
-      pop += (int)(blocks_for((long long)len + add, bs) - blocks_for(len, bs));
-      if (add > 0) blk += (len + add - 1) / bs - len / bs + 1;
+      pop += blocks_for(a, len + add) - blocks_for(a, len);
+      if (add > 0) blk += block_of(a, len + add - 1) - block_of(a, len) + 1;
     }
     if (threadIdx.x == 0) s_row[a.B] = (int)tot.y;
   }
@@ -148,21 +154,38 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(ExtendArgs a) {
   }
   const int lane = threadIdx.x & 15;
   const int groups = gridDim.x * (blockDim.x / 16);
-  for (long long u = blockIdx.x * (blockDim.x / 16) + (threadIdx.x >> 4); u < nblk; u += groups) {
-    int lo = 0, hi = a.B - 1;  // the last sequence b with s_blk[b] <= u
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (s_blk[mid] <= u) lo = mid; else hi = mid - 1;
+  constexpr int kAtOnce = 4;  // blocks of a group in flight: each waits for its number
+  for (long long u0 = blockIdx.x * (blockDim.x / 16) + (threadIdx.x >> 4); u0 < nblk;
+       u0 += (long long)groups * kAtOnce) {
+    int seq[kAtOnce], i[kAtOnce], id[kAtOnce];
+    bool fresh[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const long long u = u0 + (long long)k * groups;
+      if (u >= nblk) continue;
+      int lo = 0, hi = a.B - 1;  // the last sequence b with s_blk[b] <= u
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_blk[mid] <= u) lo = mid; else hi = mid - 1;
+      }
+      const int held = blocks_for(a, s_len[lo]);
+      seq[k] = lo;
+      i[k] = block_of(a, s_len[lo]) + (int)(u - s_blk[lo]);
+      fresh[k] = i[k] >= held;
+      id[k] = __ldcg(fresh[k] ? a.free_stack + (ft - 1 - (s_pop[lo] + i[k] - held))
+                              : a.tables + (size_t)lo * a.max_blocks + i[k]);
     }
-    const int len = s_len[lo], add = s_row[lo + 1] - s_row[lo];
-    const int held = (int)blocks_for(len, bs), i = len / bs + (int)(u - s_blk[lo]);
-    int32_t* entry = a.tables + (size_t)lo * a.max_blocks + i;
-    const int id = i < held ? *entry : a.free_stack[ft - 1 - (s_pop[lo] + i - held)];
-    if (i >= held && lane == 0) *entry = id;
-    if (!a.slot_map) continue;
-    const int first = max(len, i * bs), end = (int)min((long long)len + add, (i + 1LL) * bs);
-    for (int pos = first + lane; pos < end; pos += 16)
-      a.slot_map[s_row[lo] + pos - len] = (long long)id * bs + pos - i * bs;
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      if (u0 + (long long)k * groups >= nblk) continue;
+      if (fresh[k] && lane == 0) a.tables[(size_t)seq[k] * a.max_blocks + i[k]] = id[k];
+      if (!a.slot_map) continue;
+      const int len = s_len[seq[k]], row = s_row[seq[k]], add = s_row[seq[k] + 1] - row;
+      const int first = max(len, i[k] * bs);
+      const int end = (int)min((long long)len + add, (i[k] + 1LL) * bs);
+      for (int pos = first + lane; pos < end; pos += 16)
+        a.slot_map[row + pos - len] = (long long)id[k] * bs + pos - i[k] * bs;
+    }
   }
   if (a.slot_map)
     for (long long r = tot.y + (long long)blockIdx.x * blockDim.x + threadIdx.x; r < a.cap;
@@ -171,15 +194,15 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(ExtendArgs a) {
 }
 
 // The plan of many rows or sequences: one CTA checks everything, then takes the
-// missing blocks off the stack (sequences ascending, entries ascending) and writes
-// lengths and offsets.
+// missing blocks off the stack (sequences ascending, entries ascending), a warp per
+// sequence, and writes lengths and offsets.
 __global__ void __launch_bounds__(kExtendThreads) extend_plan_kernel(ExtendArgs a) {
   pdl_begin();
+  extern __shared__ int s_seq[];  // [B] blocks popped for the sequences before
   __shared__ int s_st0;
   if (threadIdx.x == 0) s_st0 = *(volatile int32_t*)a.status;
   __syncthreads();
   if (s_st0 != SPEC_OK) return;
-  const int bs = a.block_size;
   const int per = (a.B + blockDim.x - 1) / blockDim.x;
   const int b0 = min(a.B, (int)threadIdx.x * per), b1 = min(a.B, b0 + per);
   const int ft = *a.free_top;
@@ -189,16 +212,24 @@ __global__ void __launch_bounds__(kExtendThreads) extend_plan_kernel(ExtendArgs 
     if (threadIdx.x == 0) set_status(a.status, code);
     return;
   }
-  int k = (int)pre.x, off = (int)pre.y;
+  int pop = (int)pre.x, off = (int)pre.y;
   for (int b = b0; b < b1; ++b) {
     const int len = a.seq_lens[b], add = a.add_len[b];
-    int32_t* tab = a.tables + (size_t)b * a.max_blocks;
-    const int held = (int)blocks_for(len, bs), need = (int)blocks_for((long long)len + add, bs);
-    for (int i = held; i < need; ++i) tab[i] = a.free_stack[ft - 1 - k++];
+    s_seq[b] = pop;
+    pop += blocks_for(a, len + add) - blocks_for(a, len);
     a.row_off[b] = off;
     off += add;
-    a.new_lens[b] = len + add;
   }
+  __syncthreads();
+  for (int b = threadIdx.x >> 5; b < a.B; b += blockDim.x >> 5) {
+    const int len = a.seq_lens[b], held = blocks_for(a, len);
+    const int n = blocks_for(a, len + a.add_len[b]) - held;
+    int32_t* tab = a.tables + (size_t)b * a.max_blocks + held;
+    for (int i = threadIdx.x & 31; i < n; i += 32)
+      tab[i] = __ldcg(a.free_stack + (ft - 1 - (s_seq[b] + i)));
+  }
+  __syncthreads();  // new_lens may be seq_lens
+  for (int b = b0; b < b1; ++b) a.new_lens[b] = a.seq_lens[b] + a.add_len[b];
   if (threadIdx.x == 0) {
     a.row_off[a.B] = (int)tot.y;
     *a.new_top = ft - (int)tot.x;
@@ -220,8 +251,9 @@ __global__ void __launch_bounds__(kFillThreads) extend_fill_kernel(ExtendArgs a)
         if (a.row_off[mid] <= r) lo = mid; else hi = mid - 1;
       }
       const int pos = a.new_lens[lo] - (a.row_off[lo + 1] - (int)r);
-      slot = (long long)a.tables[(size_t)lo * a.max_blocks + pos / a.block_size] * a.block_size +
-             pos % a.block_size;
+      const int i = block_of(a, pos);
+      slot = (long long)a.tables[(size_t)lo * a.max_blocks + i] * a.block_size + pos -
+             i * a.block_size;
     }
     a.slot_map[r] = slot;
   }
@@ -280,12 +312,13 @@ __global__ void __launch_bounds__(kStoreThreads) store_kv_kernel(StoreArgs a) {
 
 }  // namespace
 
-// One launch where a cluster's CTAs do the writing in a few microseconds: up to
-// kClusterRows rows of slot map, by 8 CTAs (one for up to kOneCtaRows), and
-// sequences whose records fit its shared memory. Else a plan and a grid that fills
-// the map at the rate of the memory.
-constexpr long long kClusterRows = 1 << 20, kOneCtaRows = 8192;
-constexpr int kClusterSeqs = 8192;
+// One launch for up to kClusterRows rows of slot map (a cluster of 8 CTAs, one CTA
+// for up to kOneCtaRows): a sequence growing by a row takes 4.6 us, 256 growing by
+// up to 5 rows 6.2 us, as long as a plan and a second launch that fills the map,
+// but a launch less for the host. Else the two launches: a cluster's few SMs
+// would take longer (64 prompts of up to 4096 rows: 24 us against 11.7).
+constexpr long long kClusterRows = 8192, kOneCtaRows = 512;
+constexpr int kClusterSeqs = 4096;  // whose records fit the cluster's shared memory
 
 cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t st) {
   if (a.B <= kClusterSeqs && a.cap <= kClusterRows) {
@@ -295,7 +328,10 @@ cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t st) {
     const unsigned ctas = a.cap <= kOneCtaRows ? 1 : 8;
     return launch_pdl_cluster(extend_kernel, dim3(ctas), dim3(kExtendThreads), smem, st, ctas, a);
   }
-  cudaError_t e = launch_pdl(extend_plan_kernel, dim3(1), dim3(kExtendThreads), 0, st, a);
+  const size_t smem = (size_t)a.B * sizeof(int);
+  cudaError_t e = reserve_dyn_smem(extend_plan_kernel, smem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(extend_plan_kernel, dim3(1), dim3(kExtendThreads), smem, st, a);
   if (e != cudaSuccess || !a.slot_map || a.cap == 0) return e;
   const long long want = (a.cap + kFillThreads - 1) / kFillThreads;
   const unsigned grid = (unsigned)(want < sm_count() * 8 ? want : sm_count() * 8);

@@ -1,12 +1,14 @@
 // Arguments and launchers of the paged-cache operators: growing block tables
 // with their slot map, and storing K/V rows in the pool.
 #pragma once
+#include "attend_plan.cuh"
 #include "common.cuh"
 
 namespace specv {
 
 struct ExtendArgs {
   int B, block_size, max_blocks, num_blocks;
+  FastDiv by_bs;      // division by block_size
   int32_t* tables;
   const int32_t* seq_lens;
   const int32_t* add_len;

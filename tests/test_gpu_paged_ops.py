@@ -85,8 +85,9 @@ def test_extend_matches_the_oracle(B, bs, lo, hi, most, inplace):
                             int(got["top"]), bs, need + 2) == []
 
 
-@pytest.mark.parametrize("B,bs,most", [(3, 16, 400000), (9000, 16, 60), (8193, 1, 2),
-                                       (500, 64, 2100), (8192, 16, 127)])
+@pytest.mark.parametrize("B,bs,most", [(3, 16, 400000), (9000, 16, 60), (4097, 1, 2),
+                                       (500, 64, 2100), (4096, 16, 2), (2, 16, 4090),
+                                       (2, 16, 4096)])
 def test_extend_large(B, bs, most):
     """Around the limits between one launch and two."""
     rng = np.random.default_rng(B)
