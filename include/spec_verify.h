@@ -321,19 +321,19 @@ int spec_store_kv(const void* k, int64_t ld_k, const void* v, int64_t ld_v, int 
  *          float32; the softmax weights are rounded to dtype for the product
  *          with v.
  * row_off: int32 [B+1], not decreasing, within [0, T]. A sequence whose range
- *          is not is left out (SPEC_EDEVICE). Rows outside every range are
- *          neither read nor written.
+ *          is not is left out (SPEC_EDEVICE). Rows outside every range have no
+ *          effect and are not written.
  * q_heads: a multiple of kv_heads, at most 128 times it.
  * head_dim: a multiple of 8, at most SPEC_MAX_HEAD_DIM.
- * scale  : finite, > 0 (usually 1/sqrt(head_dim)).
+ * scale  : > 0, scale * log2(e) finite (usually 1/sqrt(head_dim)).
  * lse    : optional out float [T, q_heads] (NULL to skip): natural log of
  *          sum_j exp(scale * q_i . k_j).
  * dev_status : may be NULL. SPEC_ETIMEOUT if a bounded wait ran out (outputs
  *          are then not to be used).
  * ws     : spec_attend_workspace_bytes(head_dim) bytes, 256-byte aligned, set to
  *          zero before its first use (and after a call that recorded
- *          SPEC_ETIMEOUT); every call leaves it ready for the next, of any
- *          sizes. Calls that may overlap on the GPU (two graphs, two streams)
+ *          SPEC_ETIMEOUT); every call leaves it ready for the next, also of
+ *          another head_dim that it is large enough for. Calls that may overlap on the GPU (two graphs, two streams)
  *          need one each.
  * Where v is not finite, rows that see it get what the sum gives; so may rows
  * up to 127 keys earlier in the same sequence (a weight of 0 times it). What

@@ -50,18 +50,18 @@ struct AttendArgs {
 };
 // Forms the maps.
 cudaError_t attend_maps(AttendArgs* a);
-// Workspace bytes of the parts, for rows padded to DP columns.
+// Workspace: the counts first, in the same place for all head sizes (one
+// workspace may serve calls of several), then the parts, rows padded to DP columns.
 struct AttendWs {
-  size_t o, ml, counts, total;
+  size_t ml, o, total;
 };
 inline int attend_padded_dim(int dim) { return dim <= 64 ? 64 : 128; }
 inline AttendWs attend_ws(int dim) {
   const size_t rows = (size_t)2 * kAttendMaxCtas * 2 * kTileRows;
   AttendWs w;
-  w.o = 0;
-  w.ml = rows * attend_padded_dim(dim) * sizeof(float);
-  w.counts = w.ml + rows * sizeof(float2);
-  w.total = (w.counts + kAttendMaxCtas * sizeof(int32_t) + 255) & ~(size_t)255;
+  w.ml = (kAttendMaxCtas * sizeof(int32_t) + 255) & ~(size_t)255;
+  w.o = w.ml + rows * sizeof(float2);
+  w.total = w.o + rows * attend_padded_dim(dim) * sizeof(float);
   return w;
 }
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st);

@@ -148,7 +148,7 @@ int attend_args(const void* q, int64_t ld_q, int dtype, const int32_t* row_off, 
       q_heads < kv_heads || q_heads % kv_heads || q_heads / kv_heads > kAttendMaxGroup ||
       q_heads > (1 << 16))
     return SPEC_EINVAL;
-  if (!(scale > 0.0f) || !std::isfinite(scale)) return SPEC_EINVAL;
+  if (!(scale > 0.0f) || !std::isfinite((float)(scale * kLog2e))) return SPEC_EINVAL;
   if (B == 0 || T == 0) return SPEC_OK;
   const int64_t row = (int64_t)q_heads * head_dim;
   if (!half_rows_ok(q, ld_q, row) || !half_rows_ok(out, ld_out, row)) return SPEC_EINVAL;
@@ -176,7 +176,7 @@ int attend_args(const void* q, int64_t ld_q, int dtype, const int32_t* row_off, 
   a->status = dev_status;
   a->part_o = reinterpret_cast<float*>((char*)ws + w.o);
   a->part_ml = reinterpret_cast<float2*>((char*)ws + w.ml);
-  a->counts = reinterpret_cast<int32_t*>((char*)ws + w.counts);
+  a->counts = reinterpret_cast<int32_t*>(ws);
   a->ctas = std::min(sm_count(), kAttendMaxCtas);
   return SPEC_OK;
 }

@@ -67,7 +67,7 @@ def test_attend_prompt(lib):
                       (7, None, -1), (8, -1, -1), (8, 16385, -1), (9, -1, -1),
                       (9, (1 << 30) + 1, -1), (10, 7, -1), (10, 0, -1), (11, 0, -1), (11, 16, -1),
                       (12, 132, -1), (12, 12, -1), (12, 0, -1), (13, 0.0, -1), (13, -1.0, -1),
-                      (13, float("inf"), -1), (13, float("nan"), -1), (14, None, -1),
+                      (13, float("inf"), -1), (13, float("nan"), -1), (13, 3e38, -1), (14, None, -1),
                       (14, odd, -1), (15, 1000, -1), (18, None, -3), (18, P(0x10010), -3),
                       (19, 1000, -3)])
 

@@ -142,6 +142,34 @@ def test_prompt_same_bits_every_time_and_without_lse():
     assert torch.equal(a, b) and torch.equal(la, lb) and torch.equal(a, c)
 
 
+def test_prompt_many_short_sequences():
+    """More sequences than threads of a block, many of them empty."""
+    rng = np.random.default_rng(11)
+    lens = rng.integers(0, 4, 900).tolist()
+    q, k, v = prompt_inputs(lens, 4, 2, 64, FP, 12)
+    out, lse, st = run_prompt(q, k, v, lens)
+    assert st == 0
+    check_prompt(q, k, v, lens, out, lse, 64 ** -0.5)
+
+
+def test_no_rows_at_all():
+    q, k, v = prompt_inputs([0, 0], 2, 1, 64, BF, 13, extra=5)
+    out, lse, st = run_prompt(q, k, v, [0, 0])
+    assert st == 0 and (out == 7).all() and (lse == 7).all()
+
+
+def test_one_workspace_for_several_head_sizes():
+    """Calls of other sizes in turn on one workspace, units divided over CTAs in
+    each, give what a workspace of their own gives."""
+    ws = _capi().attend_workspace(128)
+    for rnd in range(2):
+        for lens, D in (([700, 30], 128), ([900], 64), ([256, 700], 96)):
+            q, k, v = prompt_inputs(lens, 4, 1, D, BF, 14 + D)
+            a, la, _ = run_prompt(q, k, v, lens, ws=ws)
+            b, lb, st = run_prompt(q, k, v, lens)
+            assert st == 0 and torch.equal(a, b) and torch.equal(la, lb)
+
+
 def paged_inputs(lens, bs, Hkv, D, dtype, seed, layers=2, extra=3):
     nb = sum(-(-n // bs) for n in lens) + extra
     max_blocks = max([-(-n // bs) for n in lens] + [1]) + 1
@@ -157,6 +185,7 @@ PAGED = [
     ([33, 5, 77], [0, 5, 1], 1, 3, 1, 40, BF), ([250, 129], [7, 129], 24, 6, 2, 128, BF),
     ([300], [40], 64, 7, 1, 96, FP), ([1000], [1], 128, 16, 1, 128, BF),
     ([900, 11], None, 256, 32, 1, 128, BF), ([130], [2], 3, 128, 1, 64, FP),
+    ([500, 384], [1, 50], 384, 4, 2, 120, FP), ([290], [3], 100, 4, 1, 88, BF),
 ]
 
 
