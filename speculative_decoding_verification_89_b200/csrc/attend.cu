@@ -358,6 +358,7 @@ struct Loader {
   // Table entries of 32 consecutive pages, one per lane: the group that the K
   // tiles have reached, the one before (V tiles follow) and the next one.
   int group, cur, prev, next;
+  uint64_t policy;
 
   __device__ Loader(const AttendArgs& a_, Shared* s, uint32_t t, int thread)
       : a(a_), sh(s), tiles(t), role(thread >> 5), lane(thread & 31), issued(0), land_ph(0) {}
@@ -389,6 +390,9 @@ struct Loader {
   __device__ void begin() {
     pooled = a.stage_k ? p.s.len - p.s.n : p.s.len;
     if (kMends || !a.tables || !a.box_rows || p.m == 0) return;
+    // K/V that one unit reads go first when the L2 needs room: streamed through it,
+    // they would push out the instructions (64 x 9 rows: 117 us, 128 without).
+    policy = p.two ? l2_evict_normal() : l2_evict_first();
     group = page_of(p.t0 * kTileKeys) >> 5;
     cur = entry(group * 32 + lane);
     next = entry(group * 32 + 32 + lane);
@@ -406,7 +410,7 @@ struct Loader {
     if (elect_one()) {
       if (!kMends && copies()) {
         mbar_arrive_expect_tx(bar, bytes);
-        tma_box4(dst, &a.map_q, role * 64, 0, p.h, tok0, bar);
+        tma_box4_hint(dst, &a.map_q, role * 64, 0, p.h, tok0, bar, l2_evict_first());  // read once
       } else {
         mbar_arrive(bar);
       }
@@ -450,7 +454,8 @@ struct Loader {
     if (elect_one()) {
 #pragma unroll
       for (int i = 0; i < kBoxes; ++i)
-        tma_box4(dst + i * (kTileKeys / kBoxes) * 128, map, role * 64, p.h, row, from[i], bar);
+        tma_box4_hint(dst + i * (kTileKeys / kBoxes) * 128, map, role * 64, p.h, row, from[i], bar,
+                      policy);
     }
   }
   __device__ void load_boxes(int t, int v, uint32_t dst, uint64_t* bar) {
