@@ -445,17 +445,24 @@ struct Loader {
     if (mend) land_ph ^= 1u << b;
     return true;
   }
-  template <int kBoxes>
-  __device__ void page_boxes(const void* map, uint32_t dst, int first, int row, int id,
+  // Boxes [i0, i0 + kBoxes) of a tile; lane at + i has the block of box i and, unless
+  // boxes are whole pages, its first row there. The numbers first, then all
+  // copies in a row: one at a time, each behind its own election, pages of 32
+  // rows cost 133 us where pages of 16 took 119 (64 x 9 rows).
+  template <int kBoxes, bool kWhole>
+  __device__ void page_boxes(const void* map, uint32_t dst, int i0, int at, int block, int row,
                              uint64_t* bar) {
-    int from[kBoxes];
+    int blocks[kBoxes], rows[kBoxes];
 #pragma unroll
-    for (int i = 0; i < kBoxes; ++i) from[i] = __shfl_sync(0xffffffffu, id, first + i);
+    for (int i = 0; i < kBoxes; ++i) {
+      blocks[i] = __shfl_sync(0xffffffffu, block, at + i);
+      rows[i] = kWhole ? 0 : __shfl_sync(0xffffffffu, row, at + i);
+    }
     if (elect_one()) {
 #pragma unroll
       for (int i = 0; i < kBoxes; ++i)
-        tma_box4_hint(dst + i * (kTileKeys / kBoxes) * 128, map, role * 64, p.h, row, from[i], bar,
-                      policy);
+        tma_box4_hint(dst + (i0 + i) * a.box_rows * 128, map, role * 64, p.h, rows[i], blocks[i],
+                      bar, policy);
     }
   }
   __device__ void load_boxes(int t, int v, uint32_t dst, uint64_t* bar) {
@@ -464,7 +471,7 @@ struct Loader {
       if (elect_one()) tma_box3(dst, map, role * 64, p.h, p.s.row0 + t * kTileKeys, bar);
       return;
     }
-    const int page = page_of(t * kTileKeys), g = page >> 5;
+    const int page = page_of(t * kTileKeys), g = page >> 5;  // a group holds whole tiles
     if (!v && g != group) {
       prev = cur;
       cur = next;
@@ -472,21 +479,30 @@ struct Loader {
       next = entry(g * 32 + 32 + lane);
     }
     int id = g == group ? cur : prev;
-    const int row = t * kTileKeys - page * a.block_size;  // not 0 in a page larger than a tile
-    const int boxes = kTileKeys / a.box_rows;
     const bool held = (g * 32 + lane) * (long long)a.block_size < pooled;
     if (!held || id < 0 || id >= a.num_blocks) {
-      if (held && (unsigned)(lane - (page & 31)) < (unsigned)boxes)
+      const int pages = page_of(t * kTileKeys + kTileKeys - 1) - page + 1;
+      if (held && (unsigned)(lane - (page & 31)) < (unsigned)pages)
         set_status(a.status, SPEC_EDEVICE);
       id = a.num_blocks;  // outside the tensor: zeros
     }
-    if (boxes == 8) {  // pages of 16 rows: the numbers first, then all copies in a row
-      page_boxes<8>(map, dst, page & 31, row, id, bar);
+    const int boxes = kTileKeys / a.box_rows;
+    if (a.block_size == kTileKeys / 8) {  // pages of 16 rows, without the general form's
+      page_boxes<8, true>(map, dst, 0, page & 31, id, 0, bar);  // shuffles (119 us; 124 with)
       return;
     }
+    const int key = t * kTileKeys + min(lane, boxes - 1) * a.box_rows, mine = page_of(key);
+    id = __shfl_sync(0xffffffffu, id, mine & 31);
+    const int row = key - mine * a.block_size;
+    if (boxes >= 8) {
 #pragma unroll 1
-    for (int i = 0; i < boxes; ++i)
-      page_boxes<1>(map, dst + i * a.box_rows * 128, (page & 31) + i, row, id, bar);
+      for (int i = 0; i < boxes; i += 8) page_boxes<8, false>(map, dst, i, i, id, row, bar);
+    } else if (boxes == 4) {
+      page_boxes<4, false>(map, dst, 0, 0, id, row, bar);
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < boxes; ++i) page_boxes<1, false>(map, dst, i, i, id, row, bar);
+    }
   }
   __device__ uint32_t chunk_addr(uint32_t tile, int row, int c) const {
     return tile + (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
@@ -1231,11 +1247,12 @@ EncodeFn encode_fn() {
 
 // Query rows: (column, head of the group, K/V head, row), a box holds the
 // whole tokens of a tile in the order of the tile's rows. Packed K/V rows: (column,
-// head, row), boxes of 128 rows. Pages: (column, head, row, block), boxes of a
-// whole page where its rows divide the tile, or of 128 rows where the tile's
-// rows divide the page; a box begins on a whole 1024-byte swizzle atom, so
-// pages of fewer than 8 rows are left to the row copies. Boxes have 64 columns;
-// those past the head's end are filled with zeros.
+// head, row), boxes of 128 rows. Pages: (column, head, row, block), boxes of the
+// largest power of two of rows that divides both a page and a tile, so none
+// crosses either; a box begins on a whole 1024-byte swizzle atom, so pages
+// whose rows are no multiple of 8 are left to the row copies (64 x 9 rows on pages
+// of 24: 608 us by row copies). Boxes have 64 columns; those past the head's end
+// are filled with zeros.
 cudaError_t attend_maps(AttendArgs* a) {
   const EncodeFn encode = encode_fn();
   if (!encode) return cudaErrorNotSupported;
@@ -1260,7 +1277,8 @@ cudaError_t attend_maps(AttendArgs* a) {
   }
   const int bs = a->block_size;
   a->box_rows = kTileKeys;
-  if (a->tables && bs % kTileKeys != 0) a->box_rows = (bs >= 8 && kTileKeys % bs == 0) ? bs : 0;
+  if (a->tables) a->box_rows = (bs & -bs) < kTileKeys ? (bs & -bs) : kTileKeys;
+  if (a->box_rows < 8) a->box_rows = 0;
   if (!a->box_rows) return cudaSuccess;
   for (int v = 0; v < 2; ++v) {
     const cuuint64_t dims[4] = {(cuuint64_t)a->dim, (cuuint64_t)a->kv_heads,

@@ -256,6 +256,26 @@ def test_paged_what_lies_past_the_end_is_not_seen():
     check_paged(q, pool, 0, tables, lens, [1, 1, 1], out, lse, 128 ** -0.5)
 
 
+@pytest.mark.parametrize("bs", [4, 8, 12, 24, 32, 40, 96, 128, 136, 200, 384])
+@pytest.mark.parametrize("staged", [False, True])
+def test_paged_block_sizes(bs, staged):
+    """Pages that a tile divides into copies of 8 rows up to 128 and pages left
+    to the row copies, ending and beginning inside a tile; more than 32 pages, a
+    sequence of whole pages; what no sequence holds is NaN."""
+    lens, rows = [bs * 40 + 5, 1, 10 * bs, 129], [1, 1, 4, 7]
+    pool, tables = paged_inputs(lens, bs, 2, 128, BF, 300 + bs)
+    held = torch.zeros(pool.shape[0], bs, dtype=torch.bool)
+    for b, n in enumerate(lens):
+        for p in range(n):
+            held[tables[b, p // bs], p % bs] = True
+    pool.masked_fill_(~held.cuda()[:, None, None, :, None, None], float("nan"))
+    stage = rand((4, 7, 2, 2, 2, 128), BF, 301).cuda() if staged else None
+    q = rand((sum(rows), 8, 128), BF, 302, 2.0).cuda()
+    out, lse, st = run_paged(q, pool, 1, tables, lens, rows, stage)
+    assert st == 0
+    check_paged(q, pool, 1, tables, lens, rows, out, lse, 128 ** -0.5, stage)
+
+
 def test_paged_invalid_values_are_flagged():
     """A bad length sees nothing; a bad table entry stands for zeros."""
     lens = [64, 200, -1, 40]
