@@ -333,8 +333,8 @@ int spec_store_kv(const void* k, int64_t ld_k, const void* v, int64_t ld_v, int 
  * ws     : spec_attend_workspace_bytes(head_dim) bytes, 256-byte aligned, set to
  *          zero before its first use (and after a call that recorded
  *          SPEC_ETIMEOUT); every call leaves it ready for the next, also of
- *          another head_dim that it is large enough for. Calls that may overlap on the GPU (two graphs, two streams)
- *          need one each.
+ *          another head_dim that it is large enough for. Calls that may overlap
+ *          on the GPU (two graphs, two streams) need one each.
  * Where v is not finite, rows that see it get what the sum gives; so may rows
  * up to 127 keys earlier in the same sequence (a weight of 0 times it). What
  * lies past a sequence's end never reaches it.

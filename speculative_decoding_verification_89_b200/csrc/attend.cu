@@ -4,7 +4,13 @@
 //   p~ = 2^(c s - m),  l += sum p~,  O += P~ V,  o = O / l,
 // c = scale * log2(e). The reference need not be the running maximum: it is
 // raised (and l, O scaled down) only when a maximum passes it by more than
-// 2^kSlack, so p~ stays below 2^kSlack and the scaling of O is rare.
+// kSlack, to kHead below that maximum, so p~ stays within 2^kSlack and the scaling
+// of O is rare. Scores, m, l, O and parts of divided units are float32. p~ is
+// rounded to the inputs' type for the second product, as the matrix instruction
+// takes one type for both operands: half a step of a weight, and for fp16 no
+// more than 2^-25 of a p~ (2^-32 of the row's largest) where it is subnormal,
+// which is why the reference lies kHead below the maximum; l sums the
+// unrounded p~. Outputs are rounded once more, to the type of out.
 //
 // HiSpec (gist.science summary of arXiv 2510.01336), section 2
 // "Unterstuetzung fuer Batch-Inferenz" (paged attention with block tables) and
@@ -19,6 +25,15 @@
 // place (two-byte elements over the same columns), which the next instruction
 // reads as its left operand for O += P~ V. While one warpgroup works on its
 // scores, the tensor cores form the other's.
+//
+// Times on the device, 32 query and 8 K/V heads of 128, bf16. 8192 rows: 490 us,
+// 1120 TFLOP/s (332 us at the measured 1656): a K/V tile with two query tiles takes
+// about 3600 cycles where the products alone need 2048 and the exponentials, 16 a
+// cycle, 2048; maximum, scaling, rounding and the hand-over between the two make
+// up the rest. 64 sequences of 9 staged rows over 512 to 4096 keys 120 us, one
+// row over 65000 keys 57 us: 4.9 and 4.7 TB/s (89 and 41 us at the measured 6.55
+// TB/s), bound by HBM and the gaps between units. One row over 700 keys 14.5 us:
+// launch, plan, first instruction fetches and join, one after the other.
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -34,7 +49,8 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kLoaders = 96;      // warps 9-11
 constexpr int kTmemCols = 512;    // S0 S1 O0 O1
-constexpr float kSlack = 8.0f;    // log2 of the largest p~
+constexpr float kSlack = 15.0f;   // log2 of the largest p~ (fp16 ends at 65504)
+constexpr float kHead = 7.0f;     // log2 of the largest p~ under a new reference
 
 // Buffers of one 128-row tile (Q, K or V) each; all of them serve all three.
 template <int DP>
@@ -279,8 +295,8 @@ __device__ __forceinline__ int first_tile_count(const AttendShape& shape, const 
 //   qk(w, x): scores of accumulator w with query tile x; begin_pv(): before the
 //     first pv; pv(w, first, last): weights times V.
 // Every step is written once: the code of both sides has to stay small enough
-// for the instruction cache beside the softmax warps' (unrolled by case it was
-// 376 KB, and the prompt of 8192 rows took 514 us).
+// for the instruction cache beside the softmax warps' (unrolled by case all kernels
+// were 376 KB: 64 x 9 rows took 170 us, at 100 KB 138, before later steps).
 // (The loading warps' side is Loader::fill: the same takes and gives in the
 // same order, with one place that loads.)
 template <typename Side>
@@ -336,12 +352,13 @@ __device__ __forceinline__ bool piece_program(int m, bool two, int c0, Side& sid
 // Loading: query rows, then K and V tiles in the order they are used
 // ---------------------------------------------------------------------------
 // Warp 9 copies columns 0-63 and warp 10 columns 64-127 of each tile with tiled
-// (TMA) copies: one for a query tile or 128 packed rows, one per page for the
-// pool. Warp 11 puts right what the copies of a sequence's last tiles cannot:
+// (TMA) copies: one for a query tile or 128 packed rows, one per page or part of a
+// page for the pool (row by row, as it was first, 8192 rows took 1266 us, with tiled
+// copies 796, before later steps). Warp 11 puts right what the copies of a sequence's last tiles cannot:
 // V rows past the keys are set to zero (what lies there must not reach a
 // product: a weight of 0 times a NaN) and staged rows are put in their place.
-// A tile is full when all three warps have arrived. Pages that no box fits
-// are copied row by row by all three.
+// A tile is full when all three warps have arrived. Pages whose rows are no
+// multiple of 8 are copied row by row by all three.
 template <int DP, bool kMends>
 struct Loader {
   static constexpr int kChunks = DP / 8;   // 16-byte chunks of a row
@@ -688,10 +705,10 @@ struct Loader {
 };
 
 // ---------------------------------------------------------------------------
-// Matrix instructions, issued by one lane of a warp
+// Matrix instructions, issued by one thread
 // ---------------------------------------------------------------------------
-// One thread runs all of it: between two products it is what the tensor cores
-// wait for, so it makes no votes and no elections.
+// Between two products it is what the tensor cores wait for, so it makes no
+// votes and no elections (a whole warp with elections: 8192 rows 557 us, so 519).
 template <typename T, int DP>
 struct Issuer {
   static constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
@@ -780,6 +797,8 @@ struct Issuer {
 // ---------------------------------------------------------------------------
 // Softmax and output, one thread per row
 // ---------------------------------------------------------------------------
+// A row's 128 scores are loaded at once and stay in registers through maximum,
+// exponentials and rounding; a thread needs no other's maximum or sum.
 template <typename T> struct Pack;
 template <> struct Pack<__nv_bfloat16> {
   static __device__ __forceinline__ uint32_t two(float lo, float hi) {
@@ -868,8 +887,8 @@ struct Softmax {
           fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
       const bool raise = valid && (top > m + kSlack || (m == -INFINITY && top > m));
       if (__any_sync(0xffffffffu, raise)) {
-        const float f = weight(m, fmaxf(m, top));
-        m = fmaxf(m, top);
+        const float ref = fmaxf(m, top - kHead), f = weight(m, ref);
+        m = ref;
         l *= f;
         if (!first) {  // the products up to the last tile's are in O
 #pragma unroll 1
@@ -1076,7 +1095,8 @@ struct Softmax {
 #pragma unroll 1
     for (int t = 0; t <= p.two; ++t) {
       const int rows = min(tpt, p.ntok - t * tpt) * a.group;
-      // Reads of several rows or of several parts at once: each takes about 700 cycles.
+      // Several rows or several parts in flight: with few rows every read's latency
+      // would show, once for each part.
       if (rows * (DP / 4) > 512) join_rows<8, 1>(p, t, rows);
       else join_rows<1, 8>(p, t, rows);
     }
@@ -1144,6 +1164,9 @@ struct Softmax {
   }
 };
 
+// One CTA per SM: 7 tiles of 32 KB (8 of 16 KB for heads of up to 64) fill its
+// shared memory, S0 S1 O0 O1 its tensor memory. Two accumulators, as one alone would leave
+// the tensor cores idle while its scores are worked on; a third has no room.
 template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_constant__ AttendArgs a) {
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -1178,8 +1201,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   find_run(a, sh);  // its barriers publish the above
   tc_fence_after();
   const uint32_t tiles = smem_u32(smem), tmem = sh->tmem;
-  // Of the 384 * 168 registers of the launch, 208 to each softmax thread (a row's
-  // 128 scores and their weights stay in registers), 88 to the others.
+  // Of the 384 * 168 registers of the launch, 208 to each of the 256 softmax threads
+  // (a row's 128 scores and their weights stay in registers), 88 to the 128 others.
   bool ok = true;
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");

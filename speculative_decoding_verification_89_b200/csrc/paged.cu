@@ -261,8 +261,9 @@ __global__ void __launch_bounds__(kFillThreads) extend_fill_kernel(ExtendArgs a)
 
 // K and V rows to their slots: a warp per token, up to four 16-byte vectors of
 // each row per lane in flight before the first is stored, loaded while the slot
-// is looked up. Bound by HBM (each byte read and written once): rows of 8 heads of
-// 128, 20000 tokens.
+// is looked up. Bound by HBM (each byte read and written once): 20000 rows of 8
+// heads of 128 take 26.8 us, 6.1 TB/s (25.0 us at the measured copy rate); 64 rows
+// 1.8 us, one warp's chain of two loads and a store.
 constexpr int kStoreThreads = 256;
 __global__ void __launch_bounds__(kStoreThreads) store_kv_kernel(StoreArgs a) {
   pdl_begin();

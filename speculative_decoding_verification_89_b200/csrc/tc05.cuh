@@ -127,7 +127,7 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// One box of a 3- or 4-dimensional tensor to shared memory.
+// One box of a 3-dimensional tensor to shared memory.
 __device__ __forceinline__ void tma_box3(uint32_t dst, const void* map, int x, int y, int z,
                                          uint64_t* bar) {
   asm volatile(
@@ -136,21 +136,7 @@ __device__ __forceinline__ void tma_box3(uint32_t dst, const void* map, int x, i
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
-__device__ __forceinline__ void tma_box4(uint32_t dst, const void* map, int x, int y, int z, int u,
-                                         uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(smem_u32(bar))
-      : "memory");
-}
-
-__device__ __forceinline__ void st_shared16(uint32_t dst, uint4 v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z),
-               "r"(v.w)
-               : "memory");
-}
-// The same with an L2 policy for the copied lines.
+// The same of a 4-dimensional one, with an L2 policy for the copied lines.
 __device__ __forceinline__ void tma_box4_hint(uint32_t dst, const void* map, int x, int y, int z,
                                               int u, uint64_t* bar, uint64_t policy) {
   asm volatile(
@@ -163,6 +149,11 @@ __device__ __forceinline__ uint64_t l2_evict_normal() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
   return p;
+}
+__device__ __forceinline__ void st_shared16(uint32_t dst, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
 }
 // 16 bytes to shared memory; `bytes` 0 writes zeros and reads nothing.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {

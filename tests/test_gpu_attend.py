@@ -334,3 +334,22 @@ def test_two_calls_at_once_with_a_workspace_each():
         capi.spec_attend_prompt(q, k, v, off, outs[i], st, ws[i % 2], stream=streams[i % 2])
     torch.cuda.synchronize()
     assert int(st) == 0 and all(torch.equal(o, want) for o in outs)
+
+
+def test_fp16_weights_far_below_the_largest():
+    """One key's score is 16.25 above all others (scores exact in fp16 products),
+    so theirs are weights of w = e^-16.25 = 1.47 * 2^-24 of the largest: half a
+    subnormal step, were the largest 1. Weights are kept at up to 2^7 of a new
+    reference, so each is off by at most 2^-25 / 2^7; outputs once more by 2^-11
+    relative, sums and exponentials by less than 2^-18."""
+    n, D = 256, 64
+    q, k, v = (torch.zeros(n, 1, D, dtype=FP, device="cuda") for _ in range(3))
+    q[:, 0, 0], k[0, 0, 0] = 4.0, 4.0625
+    v[1:] = 1024.0
+    out, lse, st = run_prompt(q, k, v, [n], scale=1.0)
+    w, i = np.exp(-16.25), np.arange(n)
+    want = 1024.0 * i * w / (1 + i * w)
+    got = out.double().cpu().numpy()[:, 0]
+    tol = want * (2.0 ** -32 / w + 2.0 ** -11 + 2.0 ** -18) + 2.0 ** -25
+    assert st == 0 and (np.abs(got - want[:, None]) <= tol[:, None]).all()
+    np.testing.assert_allclose(lse.cpu().numpy()[:, 0], 16.25 + np.log1p(i * w), rtol=2.0 ** -20)
