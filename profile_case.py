@@ -10,6 +10,8 @@ while the whole case stays well under a few GB of device memory.
     python profile_case.py --B 64 --vp 8
     python profile_case.py --small        (B=1, K=4, V=1024 fp32: the one-launch check)
     python profile_case.py --engine --iters 8   (rounds of the benchmark's engine loop)
+    python profile_case.py --attend  (attention: 64 x 9 staged rows over the paged cache, then
+                                      a prompt of 8192 rows)
 """
 from __future__ import annotations
 
@@ -37,6 +39,8 @@ def main():
     ap.add_argument("--draft", action="store_true", help="run the draft step instead of verifying")
     ap.add_argument("--engine", action="store_true",
                     help="--iters rounds of the engine loop (64 sequences, V=32000 bf16)")
+    ap.add_argument("--attend", action="store_true",
+                    help="paged attention of 64 x 9 staged rows, then of one prompt of 8192 rows")
     ap.add_argument("--small", action="store_true",
                     help="chain verification of B=1, K=4, V=1024 fp32 (fresh rows each call)")
     ap.add_argument("--vp", type=int, default=0,
@@ -47,6 +51,8 @@ def main():
     dev = torch.device("cuda")
     if args.small:
         return small(args, dev)
+    if args.attend:
+        return attend(args, dev)
     if args.engine:
         import bench
         r = bench.run_cfg_engine(dev, rounds=args.iters)
@@ -97,6 +103,30 @@ def main():
     print(f"B={B} status={int(st.item())} us/iter median={sorted(times)[len(times) // 2]:.1f}")
     if int(st.item()) != 0:
         raise SystemExit(1)
+
+
+def attend(args, dev):
+    """One layer: 32 query and 8 K/V heads of 128 bf16; 64 contexts of 2048 in blocks of 16."""
+    g = torch.Generator(device=dev).manual_seed(7)
+
+    def rand(*shape):
+        return torch.randn(shape, generator=g, device=dev).to(torch.bfloat16)
+
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    ws = capi.attend_workspace(128, device=dev)
+    nb = 64 * 128
+    tables = torch.randperm(nb, generator=g, device=dev).to(torch.int32).view(64, 128)
+    lens = torch.full((64,), 2048, dtype=torch.int32, device=dev)
+    pool, stage = rand(nb, 1, 2, 16, 8, 128), rand(64, 9, 1, 2, 8, 128)
+    q, out = rand(64 * 9, 32, 128), torch.empty((64 * 9, 32, 128), dtype=torch.bfloat16, device=dev)
+    qp, kp, vp = rand(8192, 32, 128), rand(8192, 8, 128), rand(8192, 8, 128)
+    op = torch.empty_like(qp)
+    off = torch.tensor([0, 8192], dtype=torch.int32, device=dev)
+    for _ in range(args.iters):
+        capi.spec_attend_paged(q, pool, 0, tables, lens, out, st, ws, kv_stage=stage)
+        capi.spec_attend_prompt(qp, kp, vp, off, op, st, ws)
+    torch.cuda.synchronize()
+    print(f"attend: {args.iters} pairs of calls, status {int(st)}")
 
 
 def small(args, dev):

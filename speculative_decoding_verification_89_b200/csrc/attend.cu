@@ -1095,71 +1095,70 @@ struct Softmax {
 #pragma unroll 1
     for (int t = 0; t <= p.two; ++t) {
       const int rows = min(tpt, p.ntok - t * tpt) * a.group;
-      // Several rows or several parts in flight: with few rows every read's latency
-      // would show, once for each part.
-      if (rows * (DP / 4) > 512) join_rows<8, 1>(p, t, rows);
-      else join_rows<1, 8>(p, t, rows);
+      // What counts is how much is in flight: a read takes about a microsecond, and
+      // one SM reads all parts. Few rows (a step of decoding) need several parts at
+      // once, 16 rows over 65536 keys in 18 parts 58.5 us where the second form
+      // took 61; many fill the reads with their columns, 256 rows over them 118 us
+      // where four columns a thread, a part at a time, took 142.
+      if (rows <= 16) join_rows<2, 8>(p, t, rows, 4);
+      else join_rows<8, 2>(p, t, rows, rows <= 64 ? 6 : 7);
     }
     return true;
   }
-  template <int kItems, int kParts>
-  __device__ __forceinline__ void join_rows(const Msg& p, int t, int rows) {
-    const int items = rows * (DP / 4);
+  // A thread has one row (of 2^log_slots), kCols groups of four columns, and reads
+  // kParts parts at once.
+  template <int kCols, int kParts>
+  __device__ __forceinline__ void join_rows(const Msg& p, int t, int rows, int log_slots) {
+    int tid;  // read here: what depends on it is not held through the tiles' loop
+    asm volatile("mov.u32 %0, %%tid.x;" : "=r"(tid));
+    const int r = tid & ((1 << log_slots) - 1);
+    if (r >= rows) return;
+    const int tk = (int)a.by_group((uint32_t)r), qh = p.h * a.group + r - tk * a.group;
+    const long long token = p.s.row0 + p.tok0 + t * a.shape.tpt + tk;
+    unsigned char* dst = a.out + token * a.ld_out + (long long)qh * a.dim * 2;
 #pragma unroll 1
-    for (int i0 = threadIdx.x; i0 < items; i0 += 256 * kItems) {
-      float m[kItems], l[kItems], o[kItems][4];
-      int c4[kItems], r[kItems];
+    for (int c = (tid >> log_slots) * kCols; c < DP / 4; c += (256 >> log_slots) * kCols) {
+      float m = -INFINITY, l = 0.0f, o[kCols][4];
 #pragma unroll
-      for (int u = 0; u < kItems; ++u) {
-        const int i = min(i0 + 256 * u, items - 1);
-        c4[u] = i / rows;
-        r[u] = i - c4[u] * rows;
-        m[u] = -INFINITY;
-        l[u] = o[u][0] = o[u][1] = o[u][2] = o[u][3] = 0.0f;
-      }
+      for (int j = 0; j < kCols; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
 #pragma unroll 1
       for (int k0 = 0; k0 < p.parts; k0 += kParts) {
-        float2 ml[kParts][kItems];
-        float4 v[kParts][kItems];
+        float2 ml[kParts];
+        float4 v[kParts][kCols];
 #pragma unroll
-        for (int k = 0; k < kParts; ++k)
+        for (int k = 0; k < kParts; ++k) {
+          const int part = min(k0 + k, p.parts - 1);
+          const long long slot = 2 * (p.head + part) + (part == 0 ? 1 : 0);
+          ml[k] = __ldcg(a.part_ml + (slot * 2 + t) * kTileRows + r);
 #pragma unroll
-          for (int u = 0; u < kItems; ++u) {
-            const int part = min(k0 + k, p.parts - 1);
-            const long long slot = 2 * (p.head + part) + (part == 0 ? 1 : 0);
-            ml[k][u] = __ldcg(a.part_ml + (slot * 2 + t) * kTileRows + r[u]);
-            v[k][u] = __ldcg(part_o(slot, t, c4[u]) + r[u]);
+          for (int j = 0; j < kCols; ++j) v[k][j] = __ldcg(part_o(slot, t, c + j) + r);
+        }
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) {
+          if (k0 + k >= p.parts) continue;
+          const float top = fmaxf(m, ml[k].x);
+          const float f = weight(m, top), g = weight(ml[k].x, top);
+          l = f * l + g * ml[k].y;
+          m = top;
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) {
+            o[j][0] = f * o[j][0] + (g == 0.0f ? 0.0f : g * v[k][j].x);
+            o[j][1] = f * o[j][1] + (g == 0.0f ? 0.0f : g * v[k][j].y);
+            o[j][2] = f * o[j][2] + (g == 0.0f ? 0.0f : g * v[k][j].z);
+            o[j][3] = f * o[j][3] + (g == 0.0f ? 0.0f : g * v[k][j].w);
           }
-#pragma unroll
-        for (int k = 0; k < kParts; ++k)
-#pragma unroll
-          for (int u = 0; u < kItems; ++u) {
-            if (k0 + k >= p.parts) continue;
-            const float top = fmaxf(m[u], ml[k][u].x);
-            const float f = weight(m[u], top), g = weight(ml[k][u].x, top);
-            l[u] = f * l[u] + g * ml[k][u].y;
-            o[u][0] = f * o[u][0] + (g == 0.0f ? 0.0f : g * v[k][u].x);
-            o[u][1] = f * o[u][1] + (g == 0.0f ? 0.0f : g * v[k][u].y);
-            o[u][2] = f * o[u][2] + (g == 0.0f ? 0.0f : g * v[k][u].z);
-            o[u][3] = f * o[u][3] + (g == 0.0f ? 0.0f : g * v[k][u].w);
-            m[u] = top;
-          }
+        }
       }
+      const bool some = l > 0.0f || l != l;
+      const float inv = some ? __fdividef(1.0f, l) : 0.0f;
 #pragma unroll
-      for (int u = 0; u < kItems; ++u) {
-        if (i0 + 256 * u >= items) continue;
-        const bool some = l[u] > 0.0f || l[u] != l[u];
-        const float inv = some ? __fdividef(1.0f, l[u]) : 0.0f;
-        const int tk = (int)a.by_group((uint32_t)r[u]), qh = p.h * a.group + r[u] - tk * a.group;
-        const long long token = p.s.row0 + p.tok0 + t * a.shape.tpt + tk;
-        if (c4[u] * 4 < a.dim)
-          *reinterpret_cast<uint2*>(a.out + token * a.ld_out +
-                                    ((long long)qh * a.dim + c4[u] * 4) * 2) =
-              make_uint2(Pack<T>::two(o[u][0] * inv, o[u][1] * inv),
-                         Pack<T>::two(o[u][2] * inv, o[u][3] * inv));
-        if (c4[u] == 0 && a.lse)
-          a.lse[token * a.q_heads + qh] = some ? (m[u] + __log2f(l[u])) * (float)kLn2 : -INFINITY;
-      }
+      for (int j = 0; j < kCols; ++j)
+        if ((c + j) * 4 < a.dim)
+          *reinterpret_cast<uint2*>(dst + (c + j) * 8) =
+              make_uint2(Pack<T>::two(o[j][0] * inv, o[j][1] * inv),
+                         Pack<T>::two(o[j][2] * inv, o[j][3] * inv));
+      if (c == 0 && a.lse)
+        a.lse[token * a.q_heads + qh] = some ? (m + __log2f(l)) * (float)kLn2 : -INFINITY;
     }
   }
 };

@@ -353,3 +353,16 @@ def test_fp16_weights_far_below_the_largest():
     tol = want * (2.0 ** -32 / w + 2.0 ** -11 + 2.0 ** -18) + 2.0 ** -25
     assert st == 0 and (np.abs(got - want[:, None]) <= tol[:, None]).all()
     np.testing.assert_allclose(lse.cpu().numpy()[:, 0], 16.25 + np.log1p(i * w), rtol=2.0 ** -20)
+
+
+@pytest.mark.parametrize("rows", [1, 2, 3, 4, 5, 8, 9, 16, 17, 32, 33, 70])
+@pytest.mark.parametrize("D", [64, 96, 128])
+def test_paged_divided_units_of_any_number_of_rows(rows, D):
+    """One sequence under one head, so every tile of keys goes to another CTA and
+    each unit is joined from as many parts: 4 query heads of 1 to 70 rows, up to
+    three units, the last of few rows."""
+    pool, tables = paged_inputs([2500], 16, 1, D, BF, 400 + rows)
+    q = rand((rows, 4, D), BF, 401, 2.0).cuda()
+    out, lse, st = run_paged(q, pool, 0, tables, [2500], [rows])
+    assert st == 0
+    check_paged(q, pool, 0, tables, [2500], [rows], out, lse, D ** -0.5)
