@@ -77,8 +77,8 @@ constexpr int kMsgs = 4;
 struct Shared {
   uint64_t msg_full[kMsgs], msg_empty[kMsgs];
   uint64_t full[8], empty[8], landed[8];
-  uint64_t s_full[2], p_full[2], o_full[2];
-  uint64_t o_empty, swap, drain;
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
+  uint64_t swap, drain;
   uint64_t parted, ticketed;
   uint32_t tmem;
   long long warp_sum[kThreads / 32];
@@ -292,8 +292,8 @@ __device__ __forceinline__ int first_tile_count(const AttendShape& shape, const 
 // two ahead. Side:
 //   take_q(w), take_k(t), take_v(t): the next buffer, for query tile w, K or V
 //     tile t; give_q(w), give_k(), give_v(): it is free once what was issued is done;
-//   qk(w, x): scores of accumulator w with query tile x; begin_pv(): before the
-//     first pv; pv(w, first, last): weights times V.
+//   qk(w, x): scores of accumulator w with query tile x; pv(w, first, last):
+//     weights times V.
 // Every step is written once: the code of both sides has to stay small enough
 // for the instruction cache beside the softmax warps' (unrolled by case all kernels
 // were 376 KB: 64 x 9 rows took 170 us, at 100 KB 138, before later steps).
@@ -308,7 +308,6 @@ __device__ __forceinline__ bool piece_program(int m, bool two, int c0, Side& sid
 #pragma unroll 1
     for (int i = -1; i < m; ++i) {
       const bool more = i + 1 < m;
-      if (i == 0 && !side.begin_pv()) return false;
       if (i >= 0) {
         if (!side.take_v(i)) return false;
         if (i < c0 && !side.pv(0, i == 0, i + 1 == c0)) return false;
@@ -332,7 +331,6 @@ __device__ __forceinline__ bool piece_program(int m, bool two, int c0, Side& sid
 #pragma unroll 1
     for (int i = -2; i < m; ++i) {
       const int w = i & 1;
-      if (i == 0 && !side.begin_pv()) return false;
       if (i >= 0) {
         if (!side.take_v(i) || !side.pv(w, i < 2, i + 2 >= m)) return false;
         side.give_v();
@@ -720,10 +718,10 @@ struct Issuer {
   Buffers<Tile<DP>::kCount> buf;
   int q0_buf, q1_buf, k_buf, v_buf;
   uint32_t p_ph;     // bit w: parity of p_full[w]
-  uint32_t pieces;   // with K/V tiles
+  uint32_t o_ph;     // bit w: parity of o_empty[w], 1 before its first use
 
   __device__ Issuer(const AttendArgs& a_, Shared* s, uint32_t t, uint32_t m)
-      : a(a_), sh(s), tiles(t), tmem(m), p_ph(0), pieces(0) {}
+      : a(a_), sh(s), tiles(t), tmem(m), p_ph(0), o_ph(3) {}
   __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t ph) {
     return wait_bar(bar, ph);
   }
@@ -757,18 +755,16 @@ struct Issuer {
     }
     tc_commit(&sh->s_full[w]);
   }
-  // The accumulators are free once the softmax warps have read the last piece's.
-  __device__ __forceinline__ bool begin_pv() {
-    if (pieces > 0 && !wait(&sh->o_empty, (pieces - 1) & 1)) return false;
-    ++pieces;
-    return true;
-  }
-  // O_w (+)= P_w V
+  // O_w (+)= P_w V, the first once the softmax warps have read the last piece's.
   __device__ __forceinline__ bool pv(int w, bool first, bool last) {
     const uint32_t vd = desc(v_buf, 128 * 128);
     const uint32_t s = tmem + w * 128, o = tmem + 256 + w * DP;
     if (!wait(&sh->p_full[w], (p_ph >> w) & 1)) return false;
     p_ph ^= 1u << w;
+    if (first) {
+      if (!wait(&sh->o_empty[w], (o_ph >> w) & 1)) return false;
+      o_ph ^= 1u << w;
+    }
     tc_fence_after();
 #pragma unroll
     for (int k = 0; k < kTileKeys / 16; ++k)
@@ -948,26 +944,86 @@ struct Softmax {
       for (int i = 0; i < 32; ++i) o[i] = f1 == 0.0f ? o[i] : fmaf(f1, __uint_as_float(x[i]), o[i]);
     }
   }
-  // A thread's 32 columns; 32-byte sectors where the rows begin on them.
-  __device__ void write_out(unsigned char* dst, int c0, const float (&o)[32]) {
-    uint32_t x[16];
+  // 16 columns of a row from col on, packed; 32-byte sectors where the rows begin on them.
+  __device__ __forceinline__ void write16(unsigned char* row, int col, const uint32_t (&x)[8]) {
+    unsigned char* d = row + col * 2;
+    if (a.out_sectors) {
+      if (col < a.dim)
+        asm volatile("st.global.L1::no_allocate.v8.b32 "
+                     "[%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d),
+                     "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]),
+                     "r"(x[7])
+                     : "memory");
+    } else {
+      if (col < a.dim) *reinterpret_cast<uint4*>(d) = make_uint4(x[0], x[1], x[2], x[3]);
+      if (col + 8 < a.dim) *reinterpret_cast<uint4*>(d + 16) = make_uint4(x[4], x[5], x[6], x[7]);
+    }
+  }
+  // The row's address in out; null for a row without a token.
+  __device__ __forceinline__ unsigned char* out_row(const Msg& p, int base, int r) const {
+    const int tk = (int)a.by_group((uint32_t)r);
+    if (tk >= min(a.shape.tpt, p.ntok - base)) return nullptr;
+    return a.out + (long long)(p.s.row0 + p.tok0 + base + tk) * a.ld_out +
+           (long long)(p.h * a.group + r - tk * a.group) * a.dim * 2;
+  }
+  // Columns [from, to) of f0 * O0 + f1 * O1 to out, all lanes. A thread holds a
+  // row, and rows lie far apart: a store would cover 32 bytes of each of 32 rows. So
+  // 64 packed columns go back to tensor memory (over columns already read) and
+  // are read as 16 rows of which 4 lanes share each: with the columns in the order
+  // of their places, a lane has 16 of the 64, and a store covers 128 bytes of 8
+  // rows (chunks of 300 to 512 rows 187 us, 196 without). Nothing reads them here,
+  // so they are not kept in the L1 (8192 rows 488 us, so 482).
+  __device__ void write_rows(const Msg& p, int base, int from, int to, uint32_t stage, bool has0,
+                             float f0, bool has1, float f1) {
+    const int lane = threadIdx.x & 31;
+    // Half of a head of 64: a row's 64 bytes by its thread. So are the zeros of a tile
+    // without keys, as the next piece's products may be in tensor memory already.
+    if (to - from < 64 || !(has0 || has1)) {
+      unsigned char* dst = out_row(p, base, row);
+#pragma unroll 1
+      for (int c = from; c < to; c += 32) {
+        float o[32];
+        read_o(c, has0, f0, has1, f1, o);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = Pack<T>::two(o[2 * i], o[2 * i + 1]);
+        for (int i = 0; i < 32; i += 16) {
+          uint32_t x[8];
 #pragma unroll
-    for (int i = 0; i < 16; i += 8) {
-      unsigned char* d = dst + (c0 + 2 * i) * 2;
-      if (a.out_sectors) {
-        if (c0 + 2 * i < a.dim)
-          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d),
-                       "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3]), "r"(x[i + 4]),
-                       "r"(x[i + 5]), "r"(x[i + 6]), "r"(x[i + 7])
-                       : "memory");
-      } else {
-        if (c0 + 2 * i < a.dim)
-          *reinterpret_cast<uint4*>(d) = make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-        if (c0 + 2 * i + 8 < a.dim)
-          *reinterpret_cast<uint4*>(d + 16) = make_uint4(x[i + 4], x[i + 5], x[i + 6], x[i + 7]);
+          for (int k = 0; k < 8; ++k) x[k] = Pack<T>::two(o[i + 2 * k], o[i + 2 * k + 1]);
+          if (dst) write16(dst, c + i, x);
+        }
       }
+      return;
+    }
+#pragma unroll 1
+    for (int c = from; c < to; c += 64) {
+      uint32_t x[32];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float o[32];
+        read_o(c + 32 * half, has0, f0, has1, f1, o);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int at = 16 * half + i;  // packed column 8 l + 2 k + e to place 8 k + 2 l + e
+          x[8 * ((at >> 1) & 3) + 2 * (at >> 3) + (at & 1)] = Pack<T>::two(o[2 * i], o[2 * i + 1]);
+        }
+      }
+      tmem_st32(stage, x, 0);
+      tmem_wait_st();
+      tmem_ld_rows16(stage, x, 0);
+      tmem_ld_rows16(stage + (16u << 16), x, 16);
+      tmem_wait_ld(x);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // rows lane / 4 + 8 j
+        unsigned char* dst = out_row(p, base, (row & ~31) + (lane >> 2) + 8 * j);
+        uint32_t y[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          y[2 * k] = x[16 * (j >> 1) + 4 * k + 2 * (j & 1)];
+          y[2 * k + 1] = x[16 * (j >> 1) + 4 * k + 2 * (j & 1) + 1];
+        }
+        if (dst) write16(dst, c + 16 * (lane & 3), y);
+      }
+      stage += 32;
     }
   }
   __device__ bool run() {
@@ -997,15 +1053,9 @@ struct Softmax {
       const long long prow = (slot * 2 + (two ? w : 0)) * kTileRows + row;
       const int r = p.s.row0 + p.tok0 + base + tok;
       const int qh = p.h * a.group + head;
-      unsigned char* dst = a.out + r * a.ld_out + (long long)qh * a.dim * 2;
       float f0 = w == 0 ? 1.0f : 0.0f, f1 = 1.0f - f0;
       int from = 0, to = DP;
       bool has0 = w == 0 && c0 > 0, has1 = w == 1 && c1 > 0;
-      for (int x = 0; x < 2; ++x)
-        if ((two ? x == w : true) && (x ? c1 : c0) > 0) {
-          if (!wait(&sh->o_full[x], o_ph[x])) return false;
-          o_ph[x] ^= 1;
-        }
       if (!two) {  // both warpgroups hold part of every row: join, half the columns each
         sh->ml[w][row] = make_float2(m, l);
         arrive(&sh->swap);
@@ -1026,6 +1076,18 @@ struct Softmax {
         from = w * (DP / 2);
         to = from + DP / 2;
       }
+      // With two query tiles a warpgroup waits for its own accumulator's barrier only:
+      // waiting for both put them in step, where one should work on scores while
+      // the other waits for products (8192 rows 482 us, so 468; 16 ragged prompts 390,
+      // 345). With one it waits for both, behind the exchange: the other warpgroup
+      // has then seen all earlier phases of its barrier, so none is taken for the
+      // one before it.
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if ((x ? c1 : c0) > 0) {
+          if ((!two || x == w) && !wait(&sh->o_full[x], o_ph[x])) return false;
+          o_ph[x] ^= 1;
+        }
       if (live) {
         tc_fence_after();
         if (whole) {
@@ -1033,16 +1095,19 @@ struct Softmax {
           f0 *= inv;
           f1 *= inv;
         }
+        if (whole) {
+          write_rows(p, base, from, to, tmem + 256 + (two ? w * DP : from), has0, f0, has1, f1);
+        } else {
 #pragma unroll 1
-        for (int c = from; c < to; c += 32) {
-          float o[32];
-          read_o(c, has0, f0, has1, f1, o);
-          if (valid && whole) write_out(dst, c, o);
-          if (valid && !whole) {
+          for (int c = from; c < to; c += 32) {
+            float o[32];
+            read_o(c, has0, f0, has1, f1, o);
             float4* po = part_o(slot, two ? w : 0, c / 4);
+            if (valid) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              po[(i / 4) * kTileRows + row] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+              for (int i = 0; i < 32; i += 4)
+                po[(i / 4) * kTileRows + row] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            }
           }
         }
         if (valid && (two || w == 0)) {
@@ -1053,13 +1118,11 @@ struct Softmax {
         }
         tc_fence_before();
       }
-      // Both accumulators' phases are waited for before either is given back, so
-      // no barrier can run two phases ahead of a waiting warp.
-      if (two && (w ? c0 : c1) > 0) {
-        if (!wait(&sh->o_full[w ^ 1], o_ph[w ^ 1])) return false;
-        o_ph[w ^ 1] ^= 1;
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) {  // eight arrivals on each accumulator's barrier
+        if (c0 > 0 && !(two && w)) mbar_arrive(&sh->o_empty[0], two ? 2 : 1);
+        if (c1 > 0 && !(two && !w)) mbar_arrive(&sh->o_empty[1], two ? 2 : 1);
       }
-      if (p.m > 0) arrive(&sh->o_empty);
       if (!whole && !join_parts(p)) return false;
     }
   }
@@ -1151,12 +1214,22 @@ struct Softmax {
       }
       const bool some = l > 0.0f || l != l;
       const float inv = some ? __fdividef(1.0f, l) : 0.0f;
+      uint32_t x[2 * kCols];
 #pragma unroll
-      for (int j = 0; j < kCols; ++j)
-        if ((c + j) * 4 < a.dim)
-          *reinterpret_cast<uint2*>(dst + (c + j) * 8) =
-              make_uint2(Pack<T>::two(o[j][0] * inv, o[j][1] * inv),
-                         Pack<T>::two(o[j][2] * inv, o[j][3] * inv));
+      for (int j = 0; j < 2 * kCols; ++j)
+        x[j] = Pack<T>::two(o[j / 2][2 * (j & 1)] * inv, o[j / 2][2 * (j & 1) + 1] * inv);
+      if constexpr (kCols >= 4) {
+#pragma unroll
+        for (int j = 0; j < 2 * kCols; j += 8) {
+          const uint32_t y[8] = {x[j],     x[j + 1], x[j + 2], x[j + 3],
+                                 x[j + 4], x[j + 5], x[j + 6], x[j + 7]};
+          write16(dst, c * 4 + 2 * j, y);
+        }
+      } else {
+        static_assert(kCols >= 4 || kCols == 2, "16 bytes");
+        if (c * 4 < a.dim)
+          *reinterpret_cast<uint4*>(dst + c * 8) = make_uint4(x[0], x[1], x[2], x[3]);
+      }
       if (c == 0 && a.lse)
         a.lse[token * a.q_heads + qh] = some ? (m + __log2f(l)) * (float)kLn2 : -INFINITY;
     }
@@ -1181,8 +1254,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       mbar_init(&sh->s_full[i], 1);
       mbar_init(&sh->p_full[i], 4);
       mbar_init(&sh->o_full[i], 1);
+      mbar_init(&sh->o_empty[i], 8);
     }
-    mbar_init(&sh->o_empty, 8);
     mbar_init(&sh->swap, 8);
     mbar_init(&sh->drain, 1);
     mbar_init(&sh->parted, 8);

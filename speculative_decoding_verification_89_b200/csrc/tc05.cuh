@@ -99,6 +99,20 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[N], const
       : SPECV_R32(r, o)
       : "r"(addr));
 }
+// 32 columns of 16 of this warp's lanes: 4 lanes of the warp share each row. Lane t
+// gets of row t / 4 columns 8 k + 2 (t % 4) and the next in r[4 k], r[4 k + 1], k < 4,
+// of row t / 4 + 8 the same in r[4 k + 2], r[4 k + 3].
+template <int N>
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t addr, uint32_t (&r)[N], const int o) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[o + 0]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]),
+        "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7]), "=r"(r[o + 8]), "=r"(r[o + 9]),
+        "=r"(r[o + 10]), "=r"(r[o + 11]), "=r"(r[o + 12]), "=r"(r[o + 13]), "=r"(r[o + 14]),
+        "=r"(r[o + 15])
+      : "r"(addr));
+}
 template <int N>
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[N], const int o) {
   asm volatile(
@@ -125,6 +139,10 @@ __device__ __forceinline__ void tmem_wait_st() {
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar, uint32_t times) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(times)
+               : "memory");
 }
 
 // One box of a 3-dimensional tensor to shared memory.
