@@ -26,13 +26,13 @@
 // reads as its left operand for O += P~ V. While one warpgroup works on its
 // scores, the tensor cores form the other's.
 //
-// Times on the device, 32 query and 8 K/V heads of 128, bf16. 8192 rows: 490 us,
-// 1120 TFLOP/s (332 us at the measured 1656): a K/V tile with two query tiles takes
-// about 3600 cycles where the products alone need 2048 and the exponentials, 16 a
+// Times on the device, 32 query and 8 K/V heads of 128, bf16. 8192 rows: 469 us,
+// 1170 TFLOP/s (332 us at the measured 1656): a K/V tile with two query tiles takes
+// about 3500 cycles where the products alone need 2048 and the exponentials, 16 a
 // cycle, 2048; maximum, scaling, rounding and the hand-over between the two make
-// up the rest. 64 sequences of 9 staged rows over 512 to 4096 keys 120 us, one
-// row over 65000 keys 57 us: 4.9 and 4.7 TB/s (89 and 41 us at the measured 6.55
-// TB/s), bound by HBM and the gaps between units. One row over 700 keys 14.5 us:
+// up the rest. 64 sequences of 9 staged rows over 512 to 4096 keys 119 us, one
+// row over 65000 keys 54 us: 4.9 TB/s both (89 and 41 us at the measured 6.55
+// TB/s), bound by HBM and the gaps between units. One row over 700 keys 12.5 us:
 // launch, plan, first instruction fetches and join, one after the other.
 #include <cuda_fp16.h>
 
@@ -526,7 +526,10 @@ struct Loader {
   // in the V rows past the keys that the copies may have filled.
   __device__ bool mend_tile(int t, int v, int b) {
     constexpr int kRows = 32 / kChunks;  // rows of a step
-    constexpr int kAhead = 4;
+    // Steps read at once: a turn takes about a microsecond (64 x 32 staged rows 136 us,
+    // 141 with 4, 132 with 8, with which 8192 rows took 479 instead of 472; 202 where
+    // rows behind the first turn were read one step at a time).
+    constexpr int kAhead = 6;
     const int c = lane % kChunks, key0 = t * kTileKeys;
     const int first = max(0, pooled - key0);             // first row not from the pool
     const int end = min(kTileKeys, p.s.len - key0);      // first row past the keys
@@ -536,26 +539,25 @@ struct Loader {
       src = (v ? a.stage_v : a.stage_k) + p.b * a.stage_seq +
             (long long)(key0 + first - pooled) * a.stage_row + ((long long)p.h * a.dim + c * 8) * 2;
     const uint32_t dst = tile(b);
-    uint4 x[kAhead];
     const int r0 = lane / kChunks;
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int r = r0 + i * kRows;
-      x[i] = r < staged && c * 8 < a.dim
-                 ? __ldg(reinterpret_cast<const uint4*>(src + r * a.stage_row))
-                 : make_uint4(0, 0, 0, 0);
-    }
-    if (!wait(&sh->landed[b], (land_ph >> b) & 1)) return false;
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int r = r0 + i * kRows;
-      if (r < staged) st_shared16(chunk_addr(dst, first + r, c), x[i]);
-    }
 #pragma unroll 1
-    for (int r = r0 + kAhead * kRows; r < staged; r += kRows)
-      st_shared16(chunk_addr(dst, first + r, c),
-                  c * 8 < a.dim ? __ldg(reinterpret_cast<const uint4*>(src + r * a.stage_row))
-                                : make_uint4(0, 0, 0, 0));
+    for (int at = r0; at == r0 || at < staged; at += kAhead * kRows) {
+      uint4 x[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int r = at + i * kRows;
+        x[i] = r < staged && c * 8 < a.dim
+                   ? __ldg(reinterpret_cast<const uint4*>(src + r * a.stage_row))
+                   : make_uint4(0, 0, 0, 0);
+      }
+      // All lanes come here at least once; their first batch waits for the copies.
+      if (at == r0 && !wait(&sh->landed[b], (land_ph >> b) & 1)) return false;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int r = at + i * kRows;
+        if (r < staged) st_shared16(chunk_addr(dst, first + r, c), x[i]);
+      }
+    }
     if (v) {
       int stop = kTileKeys;  // pages past the last are zeros already
       if (a.tables) {

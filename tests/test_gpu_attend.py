@@ -366,3 +366,24 @@ def test_paged_divided_units_of_any_number_of_rows(rows, D):
     out, lse, st = run_paged(q, pool, 0, tables, [2500], [rows])
     assert st == 0
     check_paged(q, pool, 0, tables, [2500], [rows], out, lse, D ** -0.5)
+
+
+@pytest.mark.parametrize("trial", range(8))
+@pytest.mark.parametrize("staged", [False, True])
+def test_paged_random(trial, staged):
+    """Units of one and of two tiles, without keys and with many, in one call:
+    more rows than positions, single rows, chunks; the same bits on a second run."""
+    rng = np.random.default_rng(500 + trial)
+    B = int(rng.integers(3, 30))
+    lens = rng.choice([0, 1, 5, 127, 128, 129, 700, 1500], B).tolist()
+    rows = rng.choice([0, 1, 2, 9, 33, 64, 65, 150], B).tolist() + [1]
+    lens.append(300)
+    Hkv, G, D = int(rng.integers(1, 4)), int(rng.choice([1, 2, 4, 7])), int(rng.choice([64, 80, 128]))
+    dtype = (BF, FP)[trial % 2]
+    pool, tables = paged_inputs(lens, int(rng.choice([8, 16, 24, 64])), Hkv, D, dtype, 600 + trial)
+    stage = rand((B + 1, 150, 2, 2, Hkv, D), dtype, 601).cuda() if staged else None
+    q = rand((sum(rows), Hkv * G, D), dtype, 602, 2.0).cuda()
+    out, lse, st = run_paged(q, pool, 1, tables, lens, rows, stage)
+    again, lse2, _ = run_paged(q, pool, 1, tables, lens, rows, stage)
+    assert st == 0 and torch.equal(out, again) and torch.equal(lse, lse2)
+    check_paged(q, pool, 1, tables, lens, rows, out, lse, D ** -0.5, stage)
