@@ -26,11 +26,11 @@
 // reads as its left operand for O += P~ V. While one warpgroup works on its
 // scores, the tensor cores form the other's.
 //
-// Times on the device, 32 query and 8 K/V heads of 128, bf16. 8192 rows: 469 us,
-// 1170 TFLOP/s (332 us at the measured 1656): a K/V tile with two query tiles takes
+// Times on the device, 32 query and 8 K/V heads of 128, bf16. 8192 rows: 472 us,
+// 1165 TFLOP/s (332 us at the measured 1656): a K/V tile with two query tiles takes
 // about 3500 cycles where the products alone need 2048 and the exponentials, 16 a
 // cycle, 2048; maximum, scaling, rounding and the hand-over between the two make
-// up the rest. 64 sequences of 9 staged rows over 512 to 4096 keys 119 us, one
+// up the rest. 64 sequences of 9 staged rows over 512 to 4096 keys 118 us, one
 // row over 65000 keys 54 us: 4.9 TB/s both (89 and 41 us at the measured 6.55
 // TB/s), bound by HBM and the gaps between units. One row over 700 keys 12.5 us:
 // launch, plan, first instruction fetches and join, one after the other.
