@@ -776,19 +776,21 @@ struct Issuer {
   }
   __device__ __forceinline__ bool run() {
     MsgRing ring;
+    bool ok = false;
     for (;;) {
       if (!wait(&sh->msg_full[ring.i], ring.ph)) break;
       const Msg* q = &sh->msg[ring.i];
       const int m = q->m, two = q->two, c0 = q->c0, end = q->end;
-      if (end) return true;
+      ok = end;
+      if (end) break;
       mbar_arrive(&sh->msg_empty[ring.i]);
       ring.step();
       if (!piece_program(m, two, c0, *this)) break;
     }
-    // Instructions in flight end before tensor memory is given back.
+    // Instructions in flight and their arrivals on barriers end before tensor memory
+    // is given back and the CTA ends.
     tc_commit(&sh->drain);
-    wait_bar(&sh->drain, 0);
-    return false;
+    return wait_bar(&sh->drain, 0) && ok;
   }
 };
 
