@@ -387,3 +387,32 @@ def test_paged_random(trial, staged):
     again, lse2, _ = run_paged(q, pool, 1, tables, lens, rows, stage)
     assert st == 0 and torch.equal(out, again) and torch.equal(lse, lse2)
     check_paged(q, pool, 1, tables, lens, rows, out, lse, D ** -0.5, stage)
+
+
+def test_two_streams_at_once_and_two_graphs_on_one_workspace():
+    """Calls in flight together on workspaces of their own, and two captured
+    graphs that share one replayed in turn, give what each gives alone."""
+    capi = _capi()
+    big, small = [3000, 17], [40, 900, 3]
+    a, b = prompt_inputs(big, 8, 2, 128, BF, 700), prompt_inputs(small, 4, 1, 64, FP, 710)
+    want = [run_prompt(*x, n)[0] for x, n in ((a, big), (b, small))]
+    off = [offsets(n).cuda() for n in (big, small)]
+    out = [torch.empty_like(x[0]) for x in (a, b)]
+    ws = [capi.attend_workspace(128), capi.attend_workspace(64)]
+    st, streams = _status(), [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, x in enumerate((a, b)):
+            with torch.cuda.stream(streams[i]):
+                capi.spec_attend_prompt(*x, off[i], out[i], st, ws[i])
+    torch.cuda.synchronize()
+    assert int(st) == 0 and all(torch.equal(o, w) for o, w in zip(out, want))
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    for i, x in enumerate((a, b)):
+        with torch.cuda.graph(graphs[i], stream=streams[0]):
+            capi.spec_attend_prompt(*x, off[i], out[i], st, ws[0])
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    assert int(st) == 0 and all(torch.equal(o, w) for o, w in zip(out, want))
