@@ -238,11 +238,13 @@ def _prepare_paged(c, seed):
 _kept = {}
 
 
-def _workspace(capi, dim):
-    """The attention workspace a program keeps between its calls."""
-    if dim not in _kept:
-        _kept[dim] = capi.attend_workspace(dim)
-    return _kept[dim]
+def _workspace(capi, q):
+    """The attention workspace a program keeps between its calls: one for each
+    device and stream, as calls that may overlap need one each."""
+    key = (q.get_device(), capi._stream(None), q.shape[-1])
+    if key not in _kept:
+        _kept[key] = capi.attend_workspace(q.shape[-1], device=q.device)
+    return _kept[key]
 
 
 def run(s):
@@ -263,7 +265,7 @@ def _run_own(s):
     if s["kind"] == "store":
         capi.spec_store_kv(s["k"], s["v"], s["slots"], s["pool"], s["layer"], s["status"])
         return s["pool"]
-    ws = _workspace(capi, s["q"].shape[-1])
+    ws = _workspace(capi, s["q"])
     if s["kind"] == "prompt":
         capi.spec_attend_prompt(s["q"], s["k"], s["v"], s["off"], s["out"], s["status"], ws,
                                 scale=s["scale"], lse=s["lse"])
