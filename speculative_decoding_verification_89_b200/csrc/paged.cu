@@ -262,14 +262,19 @@ __global__ void __launch_bounds__(kFillThreads) extend_fill_kernel(ExtendArgs a)
 // K and V rows to their slots: a warp per token, up to four 16-byte vectors of
 // each row per lane in flight before the first is stored, loaded while the slot
 // is looked up. Bound by HBM (each byte read and written once): 20000 rows of 8
-// heads of 128 take 26.8 us, 6.1 TB/s (25.0 us at the measured copy rate); 64 rows
-// 1.8 us, one warp's chain of two loads and a store.
+// heads of 128 take 27.4 us, 6.0 TB/s (25.0 us at the measured copy rate); 64 rows
+// 2.3 us, one warp's chain of two loads and a store, then the cluster's barrier.
 constexpr int kStoreThreads = 256;
-__global__ void __launch_bounds__(kStoreThreads) store_kv_kernel(StoreArgs a) {
-  pdl_begin();
+constexpr int kStoreRows = kStoreThreads / 32;  // rows of a CTA
+constexpr int kStoreClusterRows = 8 * kStoreRows;
+
+__device__ __forceinline__ bool bad_slot(const StoreArgs& a, long long slot) {
+  return slot < -1 || slot >= (long long)a.num_blocks * a.block_size;
+}
+
+// Row t by one warp; returns whether its slot is bad.
+__device__ __forceinline__ bool store_row(const StoreArgs& a, int t) {
   const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * (kStoreThreads / 32) + (threadIdx.x >> 5);
-  if (t >= a.T) return;
   const int st0 = a.status ? *(volatile int32_t*)a.status : SPEC_OK;
   const long long slot = a.slot_map[t];
   const uint4* k = reinterpret_cast<const uint4*>(a.k + t * a.ld_k);
@@ -282,12 +287,9 @@ __global__ void __launch_bounds__(kStoreThreads) store_kv_kernel(StoreArgs a) {
       x[u] = __ldcs(k + lane + 32 * u);
       y[u] = __ldcs(v + lane + 32 * u);
     }
-  if (st0 != SPEC_OK || slot == -1) return;
+  if (st0 != SPEC_OK || slot == -1) return false;
+  if (bad_slot(a, slot)) return true;
   const long long slots = (long long)a.num_blocks * a.block_size;
-  if (slot < -1 || slot >= slots) {
-    if (lane == 0) set_status(a.status, SPEC_EINVAL);
-    return;
-  }
   const long long block =
       slots <= INT32_MAX ? (uint32_t)slot / (uint32_t)a.block_size : slot / a.block_size;
   uint4* dst = reinterpret_cast<uint4*>(a.pool + block * a.page_bytes +
@@ -309,6 +311,37 @@ __global__ void __launch_bounds__(kStoreThreads) store_kv_kernel(StoreArgs a) {
         y[u] = __ldcs(v + i + 32 * u);
       }
   }
+  return false;
+}
+
+// A row is stored unless the status word held an error before the call, so the
+// call's own error, of a bad slot, may appear there only once every row has read
+// the word: after the barrier of the cluster that is the whole grid (up to
+// kStoreClusterRows rows), else in a launch of its own (store_flag_kernel). 64 rows
+// take 2.3 us with the barrier, 2.5 with the launch, and from Python, where the
+// host is the limit, 7.1 and 8.9.
+template <bool kCluster>
+__global__ void __launch_bounds__(kStoreThreads) store_kv_kernel(StoreArgs a) {
+  pdl_begin();
+  const int t = blockIdx.x * kStoreRows + (threadIdx.x >> 5);
+  const bool bad = t < a.T && store_row(a, t);
+  if constexpr (kCluster) {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (bad && (threadIdx.x & 31) == 0) set_status(a.status, SPEC_EINVAL);
+  }
+}
+
+// Flags bad slots after store_kv_kernel, whose CTAs have waited for all work before
+// them when they let this launch begin: the map is complete, and is read while
+// the last rows are stored.
+__global__ void __launch_bounds__(kStoreThreads) store_flag_kernel(StoreArgs a) {
+  bool bad = false;
+  for (long long t = (long long)blockIdx.x * blockDim.x + threadIdx.x; t < a.T;
+       t += (long long)gridDim.x * blockDim.x)
+    bad |= bad_slot(a, a.slot_map[t]);
+  pdl_begin();  // every row has read the status word
+  if (bad) set_status(a.status, SPEC_EINVAL);
 }
 
 }  // namespace
@@ -340,8 +373,18 @@ cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_store_kv(const StoreArgs& a, cudaStream_t st) {
-  const unsigned grid = (unsigned)((a.T + (long long)kStoreThreads / 32 - 1) / (kStoreThreads / 32));
-  return launch_pdl(store_kv_kernel, dim3(grid), dim3(kStoreThreads), 0, st, a);
+  if (a.status && a.T <= kStoreClusterRows) {
+    const unsigned ctas = a.T <= kStoreRows ? 1 : kStoreClusterRows / kStoreRows;
+    return launch_pdl_cluster(store_kv_kernel<true>, dim3(ctas), dim3(kStoreThreads), 0, st, ctas,
+                              a);
+  }
+  const unsigned grid = (unsigned)((a.T + (long long)kStoreRows - 1) / kStoreRows);
+  const cudaError_t e =
+      launch_pdl(store_kv_kernel<false>, dim3(grid), dim3(kStoreThreads), 0, st, a);
+  if (e != cudaSuccess || !a.status) return e;
+  const long long want = (a.T + (long long)kStoreThreads - 1) / kStoreThreads;
+  const unsigned flags = (unsigned)(want < sm_count() ? want : sm_count());
+  return launch_pdl(store_flag_kernel, dim3(flags), dim3(kStoreThreads), 0, st, a);
 }
 
 }  // namespace specv
