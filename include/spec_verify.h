@@ -328,12 +328,12 @@ int spec_store_kv(const void* k, int64_t ld_k, const void* v, int64_t ld_v, int 
  * scale  : > 0, scale * log2(e) finite (usually 1/sqrt(head_dim)).
  * lse    : optional out float [T, q_heads] (NULL to skip): natural log of
  *          sum_j exp(scale * q_i . k_j).
- * dev_status : may be NULL. SPEC_ETIMEOUT if a bounded wait ran out (outputs
- *          are then not to be used).
+ * dev_status : may be NULL. SPEC_ETIMEOUT if a bounded wait ran out: outputs
+ *          are then not to be used, which a caller without it cannot tell.
  * ws     : spec_attend_workspace_bytes(head_dim) bytes, 256-byte aligned, set to
- *          zero before its first use (and after a call that recorded
- *          SPEC_ETIMEOUT); every call leaves it ready for the next, also of
- *          another head_dim that it is large enough for. Calls that may overlap
+ *          zero before its first use; every call, one whose wait ran out among
+ *          them, leaves it ready for the next, also of another head_dim that it
+ *          is large enough for. Calls that may overlap
  *          on the GPU (two graphs, two streams) need one each.
  * Where v is not finite, rows that see it get what the sum gives; so may rows
  * up to 127 keys earlier in the same sequence (a weight of 0 times it). What
@@ -681,6 +681,12 @@ int spec_test_set_wait_limit_ns(uint64_t ns);
  * uncopied. Set it
  * back to 2000000000 afterwards; a device-wide setting, as above. */
 int spec_test_set_copy_wait_limit_ns(uint64_t ns);
+
+/* Test hook (no counterpart in the paper): in attention calls made from now
+ * on, CTA `cta` (each has a share of the call's K/V tiles) issues no matrix
+ * instruction, so the waits for them run out after their 2 s and the call
+ * records SPEC_ETIMEOUT. Lets a test exercise that path; -1 ends it. */
+int spec_test_stop_attend_cta(int cta);
 
 /* Test hook of spec_verify_chain_noalloc (no counterpart in the paper):
  * forgets every kept scratch address and makes the next n address lookups

@@ -76,6 +76,7 @@ _SIGS = {
     "spec_noalloc_test_fail_lookups": (_i, [_i]),
     "spec_test_set_wait_limit_ns": (_i, [_u64]),
     "spec_test_set_copy_wait_limit_ns": (_i, [_u64]),
+    "spec_test_stop_attend_cta": (_i, [_i]),
     "spec_draft_workspace_bytes": (_sz, [_i, _i, _i]),
     "spec_outcome_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
     "spec_outcome_law": (_i, [_p, _i64, _p, _i64, _i, _i, _i, _i, _p, _p, _i, _p, _p, _p, _p,
@@ -395,8 +396,8 @@ def spec_attend_workspace_bytes(head_dim):
 
 
 def attend_workspace(head_dim, device="cuda"):
-    """A zero-filled workspace tensor of the size an attention call needs; calls
-    leave it ready for the next one."""
+    """A zero-filled workspace tensor of the size an attention call needs; calls,
+    also one that recorded SPEC_ETIMEOUT, leave it ready for the next one."""
     n = spec_attend_workspace_bytes(head_dim)
     if n == 0:
         raise ValueError("invalid sizes")

@@ -86,6 +86,8 @@ struct Shared {
   int start[4];       // sequence, head, unit, cost taken of it
   long long from, run, share;  // start and cost of this CTA's run, cost of a full one
   int last;           // this CTA wrote the last part of a unit
+  int counted;        // divided pieces of this CTA's run that are counted
+  int failed;         // a wait ran out
   Msg msg[kMsgs];
   float2 ml[2][kTileRows];
 };
@@ -230,6 +232,42 @@ __device__ __forceinline__ void find_run(const AttendArgs& a, Shared* sh) {
 __device__ __forceinline__ Cursor cursor(const AttendArgs& a, const Shared* sh) {
   return Cursor(a.shape, SeqOf{&a}, a.B, a.kv_heads, sh->start[0], sh->start[1], sh->start[2],
                 sh->start[3], sh->run, sh->seq);
+}
+
+// Of a divided piece's unit: the CTA that has its first part, and how many parts.
+// The unit's place on the cost line: a later part begins with the run, a first one
+// ends with it.
+__device__ __forceinline__ long long unit_from(const Shared* sh, const AttendPiece& x) {
+  return x.t0 > 0 ? sh->from - x.t0 : sh->from + sh->run - x.t1;
+}
+__device__ __forceinline__ int unit_head(const Shared* sh, const AttendPiece& x) {
+  return (int)quotient(unit_from(sh, x), sh->share);
+}
+__device__ __forceinline__ int unit_parts(const Shared* sh, const AttendPiece& x, int head) {
+  return (int)quotient(unit_from(sh, x) + x.nt - 1, sh->share) - head + 1;
+}
+// Counts a part of the unit that CTA `head` begins; whether it was the last one, which
+// leaves the count at zero for the next call.
+__device__ __forceinline__ bool count_part(const AttendArgs& a, int head, int parts) {
+  int n;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
+               : "=r"(n)
+               : "l"(a.counts + head)
+               : "memory");
+  const bool last = n == parts - 1;
+  if (last) a.counts[head] = 0;
+  return last;
+}
+// Counts the divided pieces that a CTA did not get to, so that the counts return to
+// zero also in a call whose waits ran out. One thread, after all roles.
+__device__ __noinline__ void count_rest(const AttendArgs& a, Shared* sh) {
+  Cursor cur = cursor(a, sh);
+  AttendPiece x;
+  for (int i = 0; cur.next(&x);) {
+    if (x.t0 == 0 && x.t1 == x.nt) continue;
+    const int head = unit_head(sh, x);
+    if (i++ >= sh->counted) count_part(a, head, unit_parts(sh, x, head));
+  }
 }
 
 // The free buffers, in the order in which they will be given back: a queue of
@@ -680,11 +718,8 @@ struct Loader {
             q->c1 = two ? m : m / 2;
             q->part = x.t0 > 0 ? 1 : x.t1 < x.nt ? 2 : 0;
             if (q->part) {
-              // The unit's place on the cost line: a later part begins with the
-              // run, a first one ends with it.
-              const long long at = x.t0 > 0 ? sh->from - x.t0 : sh->from + sh->run - x.t1;
-              q->head = (int)quotient(at, sh->share);
-              q->parts = (int)quotient(at + x.nt - 1, sh->share) - q->head + 1;
+              q->head = unit_head(sh, x);
+              q->parts = unit_parts(sh, x, q->head);
             }
           }
           mbar_arrive(&sh->msg_full[out.i]);
@@ -777,7 +812,7 @@ struct Issuer {
   __device__ __forceinline__ bool run() {
     MsgRing ring;
     bool ok = false;
-    for (;;) {
+    while ((int)blockIdx.x != a.stop_cta) {
       if (!wait(&sh->msg_full[ring.i], ring.ph)) break;
       const Msg* q = &sh->msg[ring.i];
       const int m = q->m, two = q->two, c0 = q->c0, end = q->end;
@@ -1143,13 +1178,8 @@ struct Softmax {
     if (threadIdx.x < 32) {
       if (!wait(&sh->parted, part_ph)) return false;
       if (threadIdx.x == 0) {
-        int n;
-        asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
-                     : "=r"(n)
-                     : "l"(a.counts + p.head)
-                     : "memory");
-        sh->last = n == p.parts - 1;
-        if (sh->last) a.counts[p.head] = 0;
+        sh->last = count_part(a, p.head, p.parts);
+        ++sh->counted;
         mbar_arrive(&sh->ticketed);
       }
       __syncwarp();
@@ -1269,6 +1299,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       mbar_init(&sh->msg_empty[i], 8 + 1 + 2);
     }
     sh->run = 0;
+    sh->counted = sh->failed = 0;
     fence_barrier_init();
   }
   if (warp == 8) tmem_alloc(&sh->tmem, kTmemCols);
@@ -1303,13 +1334,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       ok = s.schedule();
     }
   }
-  if (!ok) set_status(a.status, SPEC_ETIMEOUT);
+  if (!ok) {
+    set_status(a.status, SPEC_ETIMEOUT);
+    sh->failed = 1;
+  }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
+    if (sh->failed && elect_one()) count_rest(a, sh);
   }
 }
 

@@ -42,6 +42,7 @@ struct AttendArgs {
   float2* part_ml;   // [2 * ctas][2 * kTileRows] (maximum in log2 units, sum)
   int32_t* counts;   // [ctas] parts written of the unit that CTA begins; 0 between calls
   int ctas;
+  int stop_cta;       // test: the CTA that issues nothing, -1 for none
   bool out_sectors;   // rows of heads in out begin on 32-byte boundaries
   // Tensors for tiled copies of 64 columns; those of K and V have box_rows rows,
   // 0: the pages fit no box and rows are copied one by one.

@@ -2,6 +2,7 @@
 // the launch sequence of each call. Declarations and the contract of every
 // entry point are in include/spec_verify.h.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -138,6 +139,8 @@ bool half_rows_ok(const void* p, int64_t ld, int64_t row) {
   return p && aligned(p, 16) && ld >= row && (ld * 2) % 16 == 0;
 }
 
+std::atomic<int> g_attend_stop_cta{-1};  // spec_test_stop_attend_cta
+
 // The checks and arguments that both attention calls share.
 int attend_args(const void* q, int64_t ld_q, int dtype, const int32_t* row_off, int B, int T,
                 int q_heads, int kv_heads, int head_dim, float scale, void* out, int64_t ld_out,
@@ -178,6 +181,7 @@ int attend_args(const void* q, int64_t ld_q, int dtype, const int32_t* row_off, 
   a->part_ml = reinterpret_cast<float2*>((char*)ws + w.ml);
   a->counts = reinterpret_cast<int32_t*>(ws);
   a->ctas = std::min(sm_count(), kAttendMaxCtas);
+  a->stop_cta = g_attend_stop_cta.load(std::memory_order_relaxed);
   return SPEC_OK;
 }
 
@@ -1026,6 +1030,12 @@ int spec_attend_paged(const void* q, int64_t ld_q, int dtype, const int32_t* row
   cudaError_t e = attend_maps(&a);
   if (e == cudaSuccess) e = launch_attend(a, (cudaStream_t)stream);
   return cuda_status(e);
+}
+
+int spec_test_stop_attend_cta(int cta) {
+  if (cta < -1) return SPEC_EINVAL;
+  g_attend_stop_cta.store(cta, std::memory_order_relaxed);
+  return SPEC_OK;
 }
 
 const char* spec_last_cuda_error(void) { return cudaGetErrorString(g_last_cuda); }
