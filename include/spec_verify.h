@@ -335,9 +335,9 @@ int spec_store_kv(const void* k, int64_t ld_k, const void* v, int64_t ld_v, int 
  *          them, leaves it ready for the next, also of another head_dim that it
  *          is large enough for. Calls that may overlap
  *          on the GPU (two graphs, two streams) need one each.
- * Where v is not finite, rows that see it get what the sum gives; so may rows
- * up to 127 keys earlier in the same sequence (a weight of 0 times it). What
- * lies past a sequence's end never reaches it.
+ * Where v is not finite, the rows that see it get an infinity or NaN in its
+ * column, and no other row gets anything of it; nor does what lies past a
+ * sequence's end reach it.
  * ------------------------------------------------------------------------- */
 size_t spec_attend_workspace_bytes(int head_dim);
 int spec_attend_prompt(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,

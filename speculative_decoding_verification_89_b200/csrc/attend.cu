@@ -88,6 +88,8 @@ struct Shared {
   int last;           // this CTA wrote the last part of a unit
   int counted;        // divided pieces of this CTA's run that are counted
   int failed;         // a wait ran out
+  int odd;            // an output is NaN
+  int joined;         // divided units joined here: 1 that of the first piece, 2 of the last
   Msg msg[kMsgs];
   float2 ml[2][kTileRows];
 };
@@ -260,7 +262,7 @@ __device__ __forceinline__ bool count_part(const AttendArgs& a, int head, int pa
 }
 // Counts the divided pieces that a CTA did not get to, so that the counts return to
 // zero also in a call whose waits ran out. One thread, after all roles.
-__device__ __noinline__ void count_rest(const AttendArgs& a, Shared* sh) {
+__device__ __forceinline__ void count_rest(const AttendArgs& a, Shared* sh) {
   Cursor cur = cursor(a, sh);
   AttendPiece x;
   for (int i = 0; cur.next(&x);) {
@@ -836,6 +838,9 @@ struct Issuer {
 // exponentials and rounding; a thread needs no other's maximum or sum.
 template <typename T> struct Pack;
 template <> struct Pack<__nv_bfloat16> {
+  static __device__ __forceinline__ float2 both(uint32_t x) {
+    return make_float2(bf_lo(x), bf_hi(x));
+  }
   static __device__ __forceinline__ uint32_t two(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -843,12 +848,33 @@ template <> struct Pack<__nv_bfloat16> {
   }
 };
 template <> struct Pack<__half> {
+  static __device__ __forceinline__ float2 both(uint32_t x) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&x));
+  }
   static __device__ __forceinline__ uint32_t two(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
   }
 };
+
+// The largest of each half as a signed number, of top and two more words of outputs:
+// 0x7fff, as which the conversions above write NaN, is larger than any other value.
+__device__ __forceinline__ uint32_t top_halves(uint32_t x, uint32_t y, uint32_t top) {
+  return __vimax3_s16x2(x, y, top);
+}
+// Sets *flag where a half of `top` (0 to 0x7fff) is NaN; without a branch, as every
+// instruction at a unit's end is fetched anew (16 ragged prompts 355 us with one).
+__device__ __forceinline__ void flag_nan(int* flag, uint32_t top) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b32 t;\n\t"
+      "add.u32 t, %1, 0x00010001;\n\t"
+      "and.b32 t, t, 0x80008000;\n\t"
+      "setp.ne.u32 p, t, 0;\n\t"
+      "@p st.shared.b32 [%0], 1;\n\t}" ::"r"(smem_u32(flag)),
+      "r"(top)
+      : "memory");
+}
 
 // Two fp32 operations per instruction.
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
@@ -872,6 +898,136 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 
 __device__ __forceinline__ float weight(float m, float ref) {
   return m == -INFINITY ? 0.0f : ex2(m - ref);
+}
+
+// The products give a row 0 times each V value that it does not see, which is NaN where
+// the value is not finite. So where an output is NaN, and the unit's tiles have such a
+// value behind the row's last key, the columns that have one are formed again, from
+// the keys that the row sees: the sum of what is not finite among their values, as no
+// weight changes that, else of the weighted values. A thread per row: such inputs
+// are rare, and only the rows of the last tiles before a value need the second.
+// (Values taken out of the tiles that not all rows of a unit see, before their
+// products, cost 16 ragged prompts 30 us; looking at the outputs costs 6.)
+template <typename T>
+__device__ void redo_row(const AttendArgs& a, const AttendPiece& x, int tok, int head) {
+  const AttendSeq& s = x.s;
+  const int seen = max(0, s.len - s.n + tok + 1), end = min(s.len, x.nt * kTileKeys);
+  const int pooled = a.stage_k ? s.len - s.n : s.len, chunks = a.dim / 8;
+  const long long qh = (long long)(x.h * a.group + head) * a.dim, at = s.row0 + tok;
+  T* out = reinterpret_cast<T*>(a.out + at * a.ld_out) + qh;
+  const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q + at * a.ld_q) + qh);
+  // K (v = 0) or V row of a key; null: a bad table entry, which stands for zeros
+  auto row = [&](int v, int key) -> const uint4* {
+    const unsigned char* p = v ? a.v : a.k;
+    const long long ld = v ? a.ld_v : a.ld_k;
+    if (key >= pooled) {
+      p = (v ? a.stage_v : a.stage_k) + x.b * a.stage_seq + (key - pooled) * a.stage_row;
+    } else if (a.tables) {
+      const int page = (int)a.by_bs((uint32_t)key);
+      const int id = a.tables[(long long)x.b * a.max_blocks + page];
+      if (id < 0 || id >= a.num_blocks) return nullptr;
+      p += id * a.page_bytes + (key - page * a.block_size) * ld;
+    } else {
+      p += (s.row0 + (long long)key) * ld;
+    }
+    return reinterpret_cast<const uint4*>(p) + x.h * chunks;
+  };
+  // Columns 32 c32 .. of a row; zeros behind the last
+  auto values = [&](const uint4* p, int c32, float (&y)[32]) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      uint4 z = make_uint4(0, 0, 0, 0);
+      if (p && 4 * c32 + g < chunks) z = p[4 * c32 + g];
+      const uint32_t w[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = Pack<T>::both(w[i]);
+        y[8 * g + 2 * i] = f.x;
+        y[8 * g + 2 * i + 1] = f.y;
+      }
+    }
+  };
+  auto score = [&](int key) {  // in log2 units
+    const uint4* k = row(0, key);
+    float sum = 0.0f;
+#pragma unroll 1
+    for (int d = 0; k && d < chunks; ++d) {
+      const uint4 u = q[d], z = k[d];
+      const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, zw[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = Pack<T>::both(uw[i]), g = Pack<T>::both(zw[i]);
+        sum = fmaf(f.x, g.x, fmaf(f.y, g.y, sum));
+      }
+    }
+    return sum * a.scale_log2;
+  };
+  float top = -INFINITY;  // of the scores, once it is needed
+#pragma unroll 1
+  for (int c32 = 0; 4 * c32 < chunks; ++c32) {
+    float y[32], o[32];
+    uint32_t bad = 0, odd = 0, nan = 0;  // columns, by bit
+    values(reinterpret_cast<const uint4*>(out), c32, y);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) odd |= (uint32_t)!isfinite(y[i]) << i;
+#pragma unroll 1
+    for (int key = seen; odd && key < end; ++key) {
+      values(row(1, key), c32, y);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) bad |= (uint32_t)!isfinite(y[i]) << i;
+    }
+    if (bad == 0) continue;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+    odd = 0;
+#pragma unroll 1
+    for (int key = 0; key < seen && (nan & bad) != bad; ++key) {
+      values(row(1, key), c32, y);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        if (isfinite(y[i])) continue;
+        o[i] += y[i];
+        odd |= 1u << i;
+        nan |= (uint32_t)(o[i] != o[i]) << i;
+      }
+    }
+    const uint32_t sums = bad & ~odd;
+    if (sums && top == -INFINITY) {
+#pragma unroll 1
+      for (int key = 0; key < seen; ++key) top = fmaxf(top, score(key));
+    }
+    float l = 0.0f;
+#pragma unroll 1
+    for (int key = 0; sums && key < seen; ++key) {
+      const float p = ex2(score(key) - (top == -INFINITY ? 0.0f : top));
+      l += p;
+      values(row(1, key), c32, y);
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (sums >> i & 1) o[i] = fmaf(p, y[i], o[i]);
+    }
+    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (bad >> i & 1) out[32 * c32 + i] = T(sums >> i & 1 ? o[i] * inv : o[i]);
+  }
+}
+// What may be left at a CTA's end, by its softmax warps: the counts of a call whose waits
+// ran out, else the rows to be formed again, of the units whose output the CTA wrote.
+template <typename T>
+__device__ __noinline__ void finish(const AttendArgs& a, Shared* sh) {
+  if (sh->failed) {
+    if (threadIdx.x == 0) count_rest(a, sh);
+    return;
+  }
+  Cursor cur = cursor(a, sh);
+  AttendPiece x;
+  while (cur.next(&x)) {
+    const bool whole = x.t0 == 0 && x.t1 == x.nt;
+    if (x.nt == 0 || !(whole || (sh->joined & (x.t0 > 0 ? 1 : 2)))) continue;
+    const int t = (int)a.by_group(threadIdx.x);
+    if (t < x.ntok) redo_row<T>(a, x, x.tok0 + t, threadIdx.x - t * a.group);
+  }
 }
 
 template <typename T, int DP>
@@ -1012,9 +1168,11 @@ struct Softmax {
   // of their places, a lane has 16 of the 64, and a store covers 128 bytes of 8
   // rows (chunks of 300 to 512 rows 187 us, 196 without). Nothing reads them here,
   // so they are not kept in the L1 (8192 rows 488 us, so 482).
+  // A valid row's NaN is flagged, for finish().
   __device__ void write_rows(const Msg& p, int base, int from, int to, uint32_t stage, bool has0,
-                             float f0, bool has1, float f1) {
+                             float f0, bool has1, float f1, bool valid) {
     const int lane = threadIdx.x & 31;
+    uint32_t top = 0;  // halves of outputs, the largest
     // Half of a head of 64: a row's 64 bytes by its thread. So are the zeros of a tile
     // without keys, as the next piece's products may be in tensor memory already.
     if (to - from < 64 || !(has0 || has1)) {
@@ -1028,9 +1186,14 @@ struct Softmax {
           uint32_t x[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) x[k] = Pack<T>::two(o[i + 2 * k], o[i + 2 * k + 1]);
+          if constexpr (DP == 64) {
+#pragma unroll
+            for (int k = 0; k < 8; k += 2) top = top_halves(x[k], x[k + 1], top);
+          }
           if (dst) write16(dst, c + i, x);
         }
       }
+      flag_nan(&sh->odd, valid ? top : 0);
       return;
     }
 #pragma unroll 1
@@ -1047,6 +1210,8 @@ struct Softmax {
         }
       }
       tmem_st32(stage, x, 0);
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) top = top_halves(x[i], x[i + 1], top);
       tmem_wait_st();
       tmem_ld_rows16(stage, x, 0);
       tmem_ld_rows16(stage + (16u << 16), x, 16);
@@ -1064,6 +1229,7 @@ struct Softmax {
       }
       stage += 32;
     }
+    flag_nan(&sh->odd, valid ? top : 0);
   }
   __device__ bool run() {
     MsgRing ring;
@@ -1135,7 +1301,7 @@ struct Softmax {
           f1 *= inv;
         }
         if (whole) {
-          write_rows(p, base, from, to, tmem + 256 + (two ? w * DP : from), has0, f0, has1, f1);
+          write_rows(p, base, from, to, tmem + 256 + (two ? w * DP : from), has0, f0, has1, f1, valid);
         } else {
 #pragma unroll 1
           for (int c = from; c < to; c += 32) {
@@ -1179,6 +1345,7 @@ struct Softmax {
       if (!wait(&sh->parted, part_ph)) return false;
       if (threadIdx.x == 0) {
         sh->last = count_part(a, p.head, p.parts);
+        if (sh->last) sh->joined |= p.part;
         ++sh->counted;
         mbar_arrive(&sh->ticketed);
       }
@@ -1252,6 +1419,10 @@ struct Softmax {
 #pragma unroll
       for (int j = 0; j < 2 * kCols; ++j)
         x[j] = Pack<T>::two(o[j / 2][2 * (j & 1)] * inv, o[j / 2][2 * (j & 1) + 1] * inv);
+      uint32_t top = 0;
+#pragma unroll
+      for (int j = 0; j < 2 * kCols; j += 2) top = top_halves(x[j], x[j + 1], top);
+      flag_nan(&sh->odd, top);
       if constexpr (kCols >= 4) {
 #pragma unroll
         for (int j = 0; j < 2 * kCols; j += 8) {
@@ -1299,7 +1470,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       mbar_init(&sh->msg_empty[i], 8 + 1 + 2);
     }
     sh->run = 0;
-    sh->counted = sh->failed = 0;
+    sh->counted = sh->failed = sh->odd = sh->joined = 0;
     fence_barrier_init();
   }
   if (warp == 8) tmem_alloc(&sh->tmem, kTmemCols);
@@ -1344,8 +1515,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
-    if (sh->failed && elect_one()) count_rest(a, sh);
   }
+  // By softmax warps, whose registers suffice for any call.
+  if (warp < 8 && (sh->failed | sh->odd)) finish<T>(a, sh);
 }
 
 template <typename T, int DP>

@@ -1,9 +1,11 @@
 """Errors of the paged-cache and attention calls on the GPU: what a bad value
 leaves done and undone, and what the next call finds."""
+import numpy as np
 import pytest
 import torch
 
-from tests.attend_run import offsets, rand
+from oracle.attend import AttendResult, attend_rows
+from tests.attend_run import check, f64, offsets, rand
 from tests.test_gpu_attend import paged_inputs
 
 pytestmark = pytest.mark.gpu
@@ -88,3 +90,96 @@ def test_attention_after_a_wait_that_ran_out(lens, rows, heads, D, cta, with_sta
         got, want = call(seed, ws), call(seed, capi.attend_workspace(D))
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
         assert got[2] == want[2] == 0
+
+
+def spoiled(length, rows, Hq, Hkv, D, dtype, bs, staged, spoil, copies=None):
+    """Attention of one sequence, there so often that a CTA takes whole units (or
+    `copies` times), with V values put in by `spoil`: every copy against the oracle.
+    bs 0: a packed prompt."""
+    capi = _capi()
+    n, group = rows or length, Hq // Hkv
+    units = -(-n // (2 * (128 // group)))
+    B = copies or 2 + 148 * 24 // (Hkv * units * (length // 128 + 4))
+    k, v = (rand((length, Hkv, D), dtype, s) for s in (30, 31))
+    spoil(v)
+    q = rand((n, Hq, D), dtype, 32, 2.0)
+    every = q.repeat(B, 1, 1).cuda()
+    out, st = torch.zeros_like(every), _status()
+    lse = torch.zeros((B * n, Hq), device="cuda")
+    ws, off = capi.attend_workspace(D), offsets([n] * B).cuda()
+    if bs == 0:
+        capi.spec_attend_prompt(every, k.repeat(B, 1, 1).cuda(), v.repeat(B, 1, 1).cuda(), off, out,
+                                st, ws, lse=lse)
+    else:
+        cached = length - n if staged else length
+        pages = max(1, -(-cached // bs))
+        pool = torch.full((2, pages * bs, Hkv, D), float("nan"), dtype=dtype)
+        pool[0, :cached], pool[1, :cached] = k[:cached], v[:cached]
+        pool = pool.view(2, pages, 1, bs, Hkv, D).permute(1, 2, 0, 3, 4, 5).contiguous().cuda()
+        stage = None
+        if staged:
+            stage = torch.stack([k[cached:], v[cached:]], 1)[None, :, None]
+            stage = stage.repeat(B, 1, 1, 1, 1, 1).cuda()
+        tables = torch.arange(pages, dtype=torch.int32).repeat(B, 1).cuda()
+        capi.spec_attend_paged(every, pool, 0, tables,
+                               torch.full((B,), cached, dtype=torch.int32).cuda(), out, st, ws,
+                               row_off=off, lse=lse, kv_stage=stage)
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    with np.errstate(invalid="ignore"):
+        want = attend_rows(f64(q), f64(k), f64(v), D ** -0.5)
+    fine = np.isfinite(want.out)
+    odd = torch.from_numpy(np.where(fine, 0.0, want.out)).to(dtype).nan_to_num(5.0, 6.0, 7.0)
+    some = ~np.isneginf(want.lse).any(1)      # rows that see a key
+    w = AttendResult(np.where(fine, want.out, 0.0)[some], want.lse[some],
+                     np.where(fine, want.mass, 0.0)[some], np.where(fine, want.vsum, 0.0)[some],
+                     want.qk[some])
+    for got, z in zip(out.view(B, n, Hq, D).cpu(), lse.view(B, n, Hq).cpu()):
+        # NaN and infinities where the sum has them, and nowhere else
+        at = torch.where(got.isfinite(), 0.0, got).nan_to_num(5.0, 6.0, 7.0)
+        assert torch.equal(at, odd)
+        check(torch.where(got.isfinite(), got, 0.0)[some], z[some], w, dtype, D)
+
+
+@pytest.mark.parametrize("length,rows,Hq,Hkv,D,dtype,bs,staged,key", [
+    (698, None, 1, 1, 64, torch.bfloat16, 0, False, 255),
+    (443, 698, 1, 1, 128, torch.bfloat16, 16, False, 255),
+    (443, 400, 4, 2, 64, torch.float16, 16, False, 383),
+    (500, None, 3, 1, 96, torch.bfloat16, 0, False, 255),
+    (700, None, 8, 2, 128, torch.float16, 0, False, 640),
+    (300, 300, 7, 1, 64, torch.bfloat16, 24, False, 200),
+    (900, 9, 32, 8, 128, torch.bfloat16, 16, True, 895),
+    (137, 9, 8, 2, 64, torch.float16, 16, True, 128),
+    (260, 260, 128, 1, 64, torch.bfloat16, 8, False, 130),
+    (300, 200, 4, 1, 80, torch.float16, 4, False, 190),
+    (210, 20, 4, 1, 128, torch.bfloat16, 3, True, 200),
+    (150, 150, 2, 1, 64, torch.bfloat16, 16, True, 149),
+    (131, None, 1, 1, 40, torch.bfloat16, 0, False, 0),
+])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("copies", [None, 1, 6])
+def test_rows_before_a_value_that_is_not_finite(length, rows, Hq, Hkv, D, dtype, bs, staged, key,
+                                                value, copies):
+    """A V value that is not finite reaches the rows that see it, in its column, and
+    no row before it, whichever tiles and parts they share."""
+    def spoil(v):
+        v[key, :, 3] = value
+    spoiled(length, rows, Hq, Hkv, D, dtype, bs, staged, spoil, copies)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("bs,staged", [(0, False), (16, False), (16, True), (4, False)])
+def test_rows_between_many_values_that_are_not_finite(dtype, bs, staged):
+    """One in every column but the first two, at positions all along, also two of
+    opposite sign in one column (NaN from the second on)."""
+    length, rows, D = 600, (None if bs == 0 else 70), 64
+    rng = np.random.default_rng(7)
+
+    def spoil(v):
+        for c in range(2, D):
+            v[int(rng.integers(0, length)), int(rng.integers(0, 2)), c] = float("inf")
+        for c in range(5, 20):
+            v[int(rng.integers(length - 70, length)), :, c] = -float("inf")
+        for c in range(40, 50):
+            v[int(rng.integers(length - 70, length)), :, c] = float("nan")
+    spoiled(length, rows, 8, 2, D, dtype, bs, staged, spoil)
