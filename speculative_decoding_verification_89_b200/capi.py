@@ -334,14 +334,16 @@ def spec_extend_paged(block_tables, seq_lens, add_len, free_stack, free_top, new
     _int_tensor(dev_status, i32, (1,), "dev_status", dev)
     _int_tensor(free_stack, i32, (num_blocks,), "free_stack", dev)
     _int_tensor(row_off, i32, (B + 1,), "row_off", dev)
-    capacity = 0
+    capacity, slots = 0, None
     if slot_map is not None:
         capacity = slot_map.numel()
         _int_tensor(slot_map, torch.int64, (capacity,), "slot_map", dev)
+        # A tensor without elements has no address; NULL would mean that there is no map.
+        slots = _ptr(slot_map) if capacity else 8
     rc = _lib.spec_extend_paged(
         B, block_size, max_blocks, _ptr(block_tables), _ptr(seq_lens), _ptr(add_len),
         _ptr(free_stack), _ptr(free_top), num_blocks, _ptr(new_lens), _ptr(new_top),
-        _ptr(row_off), _ptr(slot_map), capacity, _ptr(dev_status), _stream(stream))
+        _ptr(row_off), slots, capacity, _ptr(dev_status), _stream(stream))
     _check("spec_extend_paged", rc)
 
 

@@ -183,3 +183,28 @@ def test_rows_between_many_values_that_are_not_finite(dtype, bs, staged):
         for c in range(40, 50):
             v[int(rng.integers(length - 70, length)), :, c] = float("nan")
     spoiled(length, rows, 8, 2, D, dtype, bs, staged, spoil)
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+def test_extend_with_a_map_of_no_rows(inplace):
+    """A slot map without elements is a map of capacity 0, not no map: rows that
+    do not fit it are refused, none is what fits."""
+    capi = _capi()
+
+    def i32(v):
+        return torch.tensor(v, dtype=torch.int32, device="cuda")
+    tables, lens, top = i32([[3, -1], [-1, -1]]), i32([5, 0]), i32([4])
+    stack, st = i32([0, 1, 2, 4, 5]), _status()
+    slots = torch.empty(0, dtype=torch.int64, device="cuda")
+    new, ntop, off = (lens, top, i32([-9] * 3)) if inplace else (i32([-9] * 2), i32([-9]),
+                                                                 i32([-9] * 3))
+    before = [t.clone() for t in (tables, lens, top, new, ntop, off)]
+    capi.spec_extend_paged(tables, lens, i32([0, 1]), stack, top, new, ntop, off, st, slot_map=slots)
+    torch.cuda.synchronize()
+    assert int(st) == capi.SPEC_EINVAL
+    for t, was in zip((tables, lens, top, new, ntop, off), before):
+        assert torch.equal(t, was)
+    st.zero_()
+    capi.spec_extend_paged(tables, lens, i32([0, 0]), stack, top, new, ntop, off, st, slot_map=slots)
+    torch.cuda.synchronize()
+    assert int(st) == 0 and new.tolist() == [5, 0] and int(ntop) == 4 and off.tolist() == [0, 0, 0]
