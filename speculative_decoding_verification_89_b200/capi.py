@@ -471,6 +471,8 @@ def spec_attend_paged(q, kv_pool, layer, block_tables, seq_lens, out, dev_status
         if kv_stage.shape != (B, Kp1, layers, 2, H, D) or kv_stage.dtype is not q.dtype or \
                 kv_stage.get_device() != dev or not kv_stage.is_contiguous():
             raise ValueError("kv_stage must be contiguous [B, Kp1, layers, 2, kv_heads, head_dim]")
+        if Kp1 == 0 and T:  # without elements it has no address, which would mean none
+            raise ValueError("more rows than kv_stage holds")
     rc = _lib.spec_attend_paged(
         _ptr(q), ld_q, code, _ptr(row_off), T // B if B else 0, B, T, Hq, _ptr(kv_pool), N,
         layers, layer, bs, H, D, _ptr(block_tables), max_blocks, _ptr(seq_lens), _ptr(kv_stage),

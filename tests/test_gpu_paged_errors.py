@@ -208,3 +208,24 @@ def test_extend_with_a_map_of_no_rows(inplace):
     capi.spec_extend_paged(tables, lens, i32([0, 0]), stack, top, new, ntop, off, st, slot_map=slots)
     torch.cuda.synchronize()
     assert int(st) == 0 and new.tolist() == [5, 0] and int(ntop) == 4 and off.tolist() == [0, 0, 0]
+
+
+def test_attention_over_a_staging_buffer_of_no_rows():
+    """Rows beside a staging buffer that holds none are refused; without rows there
+    is nothing to refuse."""
+    capi = _capi()
+    pool, tables = paged_inputs([40], 16, 1, 64, torch.bfloat16, 40, layers=1)
+    lens, ws, st = torch.tensor([40], dtype=torch.int32).cuda(), capi.attend_workspace(64), _status()
+    stage = torch.empty((1, 0, 1, 2, 1, 64), dtype=torch.bfloat16, device="cuda")
+    for n, off in ((1, None), (2, offsets([2]).cuda())):
+        q = rand((n, 2, 64), torch.bfloat16, 41).cuda()
+        out = torch.full_like(q, 7.0)
+        with pytest.raises(ValueError):
+            capi.spec_attend_paged(q, pool, 0, tables.cuda(), lens, out, st, ws, row_off=off,
+                                   kv_stage=stage)
+        torch.cuda.synchronize()
+        assert (out == 7).all()
+    capi.spec_attend_paged(q[:0], pool, 0, tables.cuda(), lens, out[:0], st, ws,
+                           row_off=offsets([0]).cuda(), kv_stage=stage)
+    torch.cuda.synchronize()
+    assert int(st) == 0
