@@ -426,9 +426,9 @@ def _attend_common(q, out, lse, row_off, dev_status, ws):
         _int_tensor(row_off, torch.int32, (max(row_off.numel(), 1),), "row_off", dev)
     if dev_status is not None:
         _int_tensor(dev_status, torch.int32, (1,), "dev_status", dev)
-    if ws.get_device() != dev:
-        raise ValueError(f"the workspace must be on cuda:{dev}")
-    return code, dev, T, Hq, D, ld_q, ld_out
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"the workspace must be contiguous on cuda:{dev}")
+    return code, dev, T, Hq, D, ld_q, ld_out, ws.numel() * ws.element_size()
 
 
 def spec_attend_prompt(q, k, v, row_off, out, dev_status, ws, scale=None, lse=None, stream=None):
@@ -436,14 +436,15 @@ def spec_attend_prompt(q, k, v, row_off, out, dev_status, ws, scale=None, lse=No
     k, v [T, kv_heads, head_dim] (bfloat16 or float16, contiguous rows at any
     stride), row_off int32 [B+1]; scale defaults to head_dim ** -0.5; lse optional float32
     [T, q_heads]."""
-    code, dev, T, Hq, D, ld_q, ld_out = _attend_common(q, out, lse, row_off, dev_status, ws)
+    code, dev, T, Hq, D, ld_q, ld_out, ws_bytes = _attend_common(q, out, lse, row_off,
+                                                                 dev_status, ws)
     shape = (T, k.shape[1], D)
     ld_k = _token_rows(k, shape, q.dtype, dev, "k")
     ld_v = _token_rows(v, shape, q.dtype, dev, "v")
     rc = _lib.spec_attend_prompt(
         _ptr(q), ld_q, _ptr(k), ld_k, _ptr(v), ld_v, code, _ptr(row_off), row_off.numel() - 1, T,
         Hq, k.shape[1], D, D ** -0.5 if scale is None else scale, _ptr(out), ld_out, _ptr(lse),
-        _ptr(dev_status), _ptr(ws), ws.numel(), _stream(stream))
+        _ptr(dev_status), _ptr(ws), ws_bytes, _stream(stream))
     _check("spec_attend_prompt", rc)
 
 
@@ -454,7 +455,8 @@ def spec_attend_paged(q, kv_pool, layer, block_tables, seq_lens, out, dev_status
     same number of rows for each sequence; kv_pool as for spec_commit_paged;
     kv_stage [B, Kp1, layers, 2, kv_heads, head_dim] if the new rows' K/V are
     staged, None if seq_lens counts them already."""
-    code, dev, T, Hq, D, ld_q, ld_out = _attend_common(q, out, lse, row_off, dev_status, ws)
+    code, dev, T, Hq, D, ld_q, ld_out, ws_bytes = _attend_common(q, out, lse, row_off,
+                                                                 dev_status, ws)
     N, layers, bs, H, Dp = _pool_sizes(kv_pool, layer, q.dtype, dev)
     if Dp != D:
         raise ValueError("q and kv_pool have different head sizes")
@@ -477,7 +479,7 @@ def spec_attend_paged(q, kv_pool, layer, block_tables, seq_lens, out, dev_status
         _ptr(q), ld_q, code, _ptr(row_off), T // B if B else 0, B, T, Hq, _ptr(kv_pool), N,
         layers, layer, bs, H, D, _ptr(block_tables), max_blocks, _ptr(seq_lens), _ptr(kv_stage),
         Kp1, D ** -0.5 if scale is None else scale, _ptr(out), ld_out, _ptr(lse),
-        _ptr(dev_status), _ptr(ws), ws.numel(), _stream(stream))
+        _ptr(dev_status), _ptr(ws), ws_bytes, _stream(stream))
     _check("spec_attend_paged", rc)
 
 

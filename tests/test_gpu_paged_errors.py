@@ -199,13 +199,15 @@ def test_extend_with_a_map_of_no_rows(inplace):
     new, ntop, off = (lens, top, i32([-9] * 3)) if inplace else (i32([-9] * 2), i32([-9]),
                                                                  i32([-9] * 3))
     before = [t.clone() for t in (tables, lens, top, new, ntop, off)]
-    capi.spec_extend_paged(tables, lens, i32([0, 1]), stack, top, new, ntop, off, st, slot_map=slots)
+    capi.spec_extend_paged(tables, lens, i32([0, 1]), stack, top, new, ntop, off, st,
+                           slot_map=slots)
     torch.cuda.synchronize()
     assert int(st) == capi.SPEC_EINVAL
     for t, was in zip((tables, lens, top, new, ntop, off), before):
         assert torch.equal(t, was)
     st.zero_()
-    capi.spec_extend_paged(tables, lens, i32([0, 0]), stack, top, new, ntop, off, st, slot_map=slots)
+    capi.spec_extend_paged(tables, lens, i32([0, 0]), stack, top, new, ntop, off, st,
+                           slot_map=slots)
     torch.cuda.synchronize()
     assert int(st) == 0 and new.tolist() == [5, 0] and int(ntop) == 4 and off.tolist() == [0, 0, 0]
 
@@ -215,7 +217,8 @@ def test_attention_over_a_staging_buffer_of_no_rows():
     is nothing to refuse."""
     capi = _capi()
     pool, tables = paged_inputs([40], 16, 1, 64, torch.bfloat16, 40, layers=1)
-    lens, ws, st = torch.tensor([40], dtype=torch.int32).cuda(), capi.attend_workspace(64), _status()
+    lens, ws = torch.tensor([40], dtype=torch.int32).cuda(), capi.attend_workspace(64)
+    st = _status()
     stage = torch.empty((1, 0, 1, 2, 1, 64), dtype=torch.bfloat16, device="cuda")
     for n, off in ((1, None), (2, offsets([2]).cuda())):
         q = rand((n, 2, 64), torch.bfloat16, 41).cuda()
@@ -229,3 +232,28 @@ def test_attention_over_a_staging_buffer_of_no_rows():
                            row_off=offsets([0]).cuda(), kv_stage=stage)
     torch.cuda.synchronize()
     assert int(st) == 0
+
+
+def test_attention_workspaces_that_are_refused():
+    """A workspace whose elements do not lie one after another has less memory than
+    elements; one of another type counts by its bytes."""
+    capi = _capi()
+    q, k = (rand((5, 2, 64), torch.bfloat16, s).cuda() for s in (50, 51))
+    out, st, off = torch.full_like(q, 7.0), _status(), offsets([5]).cuda()
+    n = capi.spec_attend_workspace_bytes(64)
+    small, ints = torch.zeros(256, dtype=torch.uint8, device="cuda"), n // 4
+    for ws in (small[:1].expand(n), torch.zeros(2 * n, dtype=torch.uint8, device="cuda")[::2],
+               torch.zeros((n // 256, 512), dtype=torch.uint8, device="cuda")[:, :256]):
+        with pytest.raises(ValueError):
+            capi.spec_attend_prompt(q, k, k, off, out, st, ws)
+    with pytest.raises(capi.SpecError):
+        capi.spec_attend_prompt(q, k, k, off, out, st,
+                                torch.zeros(ints - 1, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert (out == 7).all() and int(st) == 0
+    want = torch.empty_like(q)
+    capi.spec_attend_prompt(q, k, k, off, want, st, capi.attend_workspace(64))
+    capi.spec_attend_prompt(q, k, k, off, out, st,
+                            torch.zeros(ints, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and int(st) == 0
