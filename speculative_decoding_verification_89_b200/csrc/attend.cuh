@@ -9,7 +9,6 @@ namespace specv {
 
 constexpr int kAttendMaxCtas = 148;
 constexpr int kAttendMaxGroup = kTileRows;  // query heads that share a K/V head
-constexpr int kAttendMaxDim = 128;
 
 struct AttendArgs {
   int B, T, q_heads, kv_heads, group, dim;
