@@ -257,3 +257,57 @@ def test_attention_workspaces_that_are_refused():
                             torch.zeros(ints, dtype=torch.int32, device="cuda"))
     torch.cuda.synchronize()
     assert torch.equal(out, want) and int(st) == 0
+
+
+@pytest.mark.parametrize("T", [40, 200, 9000])
+def test_the_cache_calls_captured_and_replayed(T):
+    """Tables grown, rows stored and attended in one captured graph, replayed with
+    other counts and values: one launch and two of each call, error pending or not."""
+    capi = _capi()
+    B, H, D, bs, cap = 3, 1, 64, 16, T
+    N = B * (-(-T // bs)) + 4
+
+    def i32(v):
+        return torch.tensor(v, dtype=torch.int32, device="cuda")
+    tables = torch.full((B, N), -1, dtype=torch.int32, device="cuda")
+    lens, top = i32([0] * B), i32([N])
+    stack, add, st = torch.randperm(N).to(torch.int32).cuda(), i32([0] * B), _status()
+    off, slots = i32([0] * (B + 1)), torch.zeros(cap, dtype=torch.int64, device="cuda")
+    kv = torch.zeros((cap, 2, H, D), dtype=torch.bfloat16, device="cuda")
+    q = rand((cap, 2, D), torch.bfloat16, 60, 2.0).cuda()
+    pool = torch.zeros((N, 1, 2, bs, H, D), dtype=torch.bfloat16, device="cuda")
+    out, ws = torch.zeros_like(q), capi.attend_workspace(D)
+
+    def calls():
+        capi.spec_extend_paged(tables, lens, add, stack, top, lens, top, off, st, slot_map=slots)
+        capi.spec_store_kv(kv[:, 0], kv[:, 1], slots, pool, 0, st)
+        capi.spec_attend_paged(q, pool, 0, tables, lens, out, st, ws, row_off=off)
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=stream):
+        calls()
+    rows = [[torch.empty((0, H, D), dtype=torch.bfloat16)] * 2 for _ in range(B)]
+    for step, n in enumerate(([T // 4, 1, T // 8], [0, T // 3, 2], [1, 1, 1])):
+        new = rand((cap, 2, H, D), torch.bfloat16, 61 + step)
+        kv.copy_(new)
+        add.copy_(torch.tensor(n))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert int(st) == 0
+        at = np.concatenate([[0], np.cumsum(n)])
+        assert off.tolist() == at.tolist() and (slots[at[-1]:] == -1).all()
+        for b in range(B):
+            r = slice(at[b], at[b + 1])
+            rows[b] = [torch.cat([x, new[r, i]]) for i, x in enumerate(rows[b])]
+            assert int(lens[b]) == len(rows[b][0])
+            some = slice(max(at[b], at[b + 1] - 5), at[b + 1])   # the last rows of each
+            want = attend_rows(f64(q[some]), *(f64(x) for x in rows[b]), D ** -0.5)
+            check(out[some], None, want, torch.bfloat16, D)
+    st.fill_(capi.SPEC_ENOBLOCKS)                       # pending: the cache stays
+    before = [t.clone() for t in (tables, lens, top, pool)]
+    kv.fill_(1.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    for t, was in zip((tables, lens, top, pool), before):
+        assert torch.equal(t, was)
+    assert int(st) == capi.SPEC_ENOBLOCKS
