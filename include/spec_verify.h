@@ -337,7 +337,8 @@ int spec_store_kv(const void* k, int64_t ld_k, const void* v, int64_t ld_v, int 
  *          on the GPU (two graphs, two streams) need one each.
  * Where v is not finite, the rows that see it get an infinity or NaN in its
  * column, and no other row gets anything of it; nor does what lies past a
- * sequence's end reach it.
+ * sequence's end reach it. (A call with such values takes longer: rows shortly
+ * before one are formed a second time.)
  * ------------------------------------------------------------------------- */
 size_t spec_attend_workspace_bytes(int head_dim);
 int spec_attend_prompt(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,

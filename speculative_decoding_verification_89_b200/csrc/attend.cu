@@ -901,23 +901,33 @@ __device__ __forceinline__ float weight(float m, float ref) {
 }
 
 // The products give a row 0 times each V value that it does not see, which is NaN where
-// the value is not finite. So where an output is NaN, and the unit's tiles have such a
-// value behind the row's last key, the columns that have one are formed again, from
-// the keys that the row sees: the sum of what is not finite among their values, as no
-// weight changes that, else of the weighted values. A thread per row: such inputs
-// are rare, and only the rows of the last tiles before a value need the second.
+// the value is not finite. So where an output is NaN, the CTA looks at its end for
+// such values, and a row with one behind its last key in its unit's tiles gets those
+// columns again, from the keys that it sees: what is not finite among their values,
+// as no weight changes that, else the sum of the weighted values, which only rows of
+// the last tiles before the first such value need. All 256 threads look, a warp
+// forms four rows at once, a key per lane: 8192 rows with one NaN near their end take
+// 40 ms (350 with a thread per row), with all values infinite 2.5 (122).
 // (Values taken out of the tiles that not all rows of a unit see, before their
-// products, cost 16 ragged prompts 30 us; looking at the outputs costs 6.)
-template <typename T>
-__device__ void redo_row(const AttendArgs& a, const AttendPiece& x, int tok, int head) {
-  const AttendSeq& s = x.s;
-  const int seen = max(0, s.len - s.n + tok + 1), end = min(s.len, x.nt * kTileKeys);
-  const int pooled = a.stage_k ? s.len - s.n : s.len, chunks = a.dim / 8;
-  const long long qh = (long long)(x.h * a.group + head) * a.dim, at = s.row0 + tok;
-  T* out = reinterpret_cast<T*>(a.out + at * a.ld_out) + qh;
-  const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q + at * a.ld_q) + qh);
+// products, cost 16 ragged prompts 30 us; looking at the outputs costs 10.)
+template <typename T, int DP>
+struct Redo {
+  static constexpr int kCols = DP / 32;  // columns of a lane
+  static constexpr int kRows = 4;        // rows of a warp at once
+  static constexpr int kStride = DP * 2 + 16;  // of rows in shared memory: eight lanes'
+                                               // 16 bytes lie in different banks
+  static_assert(8 * (kRows + 32) * kStride <= Tile<DP>::kSmemTiles, "scratch");
+  const AttendArgs& a;
+  Shared* sh;
+  AttendPiece x;
+  // Of each column, in place of the softmax warps' exchange: the first key with NaN, an
+  // infinity, a negative one; the last with any of them that not all rows see.
+  __device__ int* first(int kind) const { return reinterpret_cast<int*>(sh->ml) + kind * 128; }
+  __device__ int* last() const { return first(3); }
+  __device__ void barrier() const { asm volatile("bar.sync 1, 256;" ::: "memory"); }
   // K (v = 0) or V row of a key; null: a bad table entry, which stands for zeros
-  auto row = [&](int v, int key) -> const uint4* {
+  __device__ const unsigned char* row(int v, int key) const {
+    const int pooled = a.stage_k ? x.s.len - x.s.n : x.s.len;
     const unsigned char* p = v ? a.v : a.k;
     const long long ld = v ? a.ld_v : a.ld_k;
     if (key >= pooled) {
@@ -928,105 +938,216 @@ __device__ void redo_row(const AttendArgs& a, const AttendPiece& x, int tok, int
       if (id < 0 || id >= a.num_blocks) return nullptr;
       p += id * a.page_bytes + (key - page * a.block_size) * ld;
     } else {
-      p += (s.row0 + (long long)key) * ld;
+      p += (x.s.row0 + (long long)key) * ld;
     }
-    return reinterpret_cast<const uint4*>(p) + x.h * chunks;
-  };
-  // Columns 32 c32 .. of a row; zeros behind the last
-  auto values = [&](const uint4* p, int c32, float (&y)[32]) {
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      uint4 z = make_uint4(0, 0, 0, 0);
-      if (p && 4 * c32 + g < chunks) z = p[4 * c32 + g];
-      const uint32_t w[4] = {z.x, z.y, z.z, z.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = Pack<T>::both(w[i]);
-        y[8 * g + 2 * i] = f.x;
-        y[8 * g + 2 * i + 1] = f.y;
-      }
-    }
-  };
-  auto score = [&](int key) {  // in log2 units
-    const uint4* k = row(0, key);
-    float sum = 0.0f;
-#pragma unroll 1
-    for (int d = 0; k && d < chunks; ++d) {
-      const uint4 u = q[d], z = k[d];
-      const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, zw[4] = {z.x, z.y, z.z, z.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = Pack<T>::both(uw[i]), g = Pack<T>::both(zw[i]);
-        sum = fmaf(f.x, g.x, fmaf(f.y, g.y, sum));
-      }
-    }
-    return sum * a.scale_log2;
-  };
-  float top = -INFINITY;  // of the scores, once it is needed
-#pragma unroll 1
-  for (int c32 = 0; 4 * c32 < chunks; ++c32) {
-    float y[32], o[32];
-    uint32_t bad = 0, odd = 0, nan = 0;  // columns, by bit
-    values(reinterpret_cast<const uint4*>(out), c32, y);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) odd |= (uint32_t)!isfinite(y[i]) << i;
-#pragma unroll 1
-    for (int key = seen; odd && key < end; ++key) {
-      values(row(1, key), c32, y);
-#pragma unroll
-      for (int i = 0; i < 32; ++i) bad |= (uint32_t)!isfinite(y[i]) << i;
-    }
-    if (bad == 0) continue;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) o[i] = 0.0f;
-    odd = 0;
-#pragma unroll 1
-    for (int key = 0; key < seen && (nan & bad) != bad; ++key) {
-      values(row(1, key), c32, y);
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        if (isfinite(y[i])) continue;
-        o[i] += y[i];
-        odd |= 1u << i;
-        nan |= (uint32_t)(o[i] != o[i]) << i;
-      }
-    }
-    const uint32_t sums = bad & ~odd;
-    if (sums && top == -INFINITY) {
-#pragma unroll 1
-      for (int key = 0; key < seen; ++key) top = fmaxf(top, score(key));
-    }
-    float l = 0.0f;
-#pragma unroll 1
-    for (int key = 0; sums && key < seen; ++key) {
-      const float p = ex2(score(key) - (top == -INFINITY ? 0.0f : top));
-      l += p;
-      values(row(1, key), c32, y);
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (sums >> i & 1) o[i] = fmaf(p, y[i], o[i]);
-    }
-    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (bad >> i & 1) out[32 * c32 + i] = T(sums >> i & 1 ? o[i] * inv : o[i]);
+    return p + (long long)x.h * a.dim * 2;
   }
-}
+  // Notes what is not finite in V rows [from, to); early: all rows see them.
+  __device__ void look(int from, int to, bool early) {
+    constexpr int kChunks = DP / 8, kStep = 256 / kChunks, kAhead = 4;
+    const int c = threadIdx.x % kChunks;
+    uint32_t seen[3] = {0, 0, 0};  // columns of the chunk with NaN, ...
+#pragma unroll 1
+    for (int at = from + threadIdx.x / kChunks; at < to; at += kAhead * kStep) {
+      uint4 z[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int key = at + k * kStep;
+        const unsigned char* v = key < to && c * 8 < a.dim ? row(1, key) : nullptr;
+        z[k] = load(reinterpret_cast<const uint4*>(v) + c, v);
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const uint32_t w[4] = {z[k].x, z[k].y, z[k].z, z[k].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 f = Pack<T>::both(w[i / 2]);
+          const float y = i % 2 ? f.y : f.x;
+          if (isfinite(y)) continue;
+          const int kind = y != y ? 0 : y > 0 ? 1 : 2, key = early ? 0 : at + k * kStep;
+          if (early) {
+            if (seen[kind] >> i & 1) continue;
+            seen[0] |= (uint32_t)(kind == 0) << i;
+            seen[1] |= (uint32_t)(kind == 1) << i;
+            seen[2] |= (uint32_t)(kind == 2) << i;
+          } else {
+            atomicMax(last() + c * 8 + i, key);
+          }
+          atomicMin(first(kind) + c * 8 + i, key);
+        }
+      }
+    }
+  }
+  // 16 bytes, or zeros: without a branch, so that several are in flight.
+  __device__ uint4 load(const uint4* p, bool there) const {
+    const uint4 z = *(there ? p : reinterpret_cast<const uint4*>(a.v));
+    return there ? z : make_uint4(0, 0, 0, 0);
+  }
+  // `n` rows at the addresses that lanes 0 .. n-1 hold (0: zeros) to dst, zeros behind
+  // the last column.
+  template <int n>
+  __device__ void copy(unsigned long long src, unsigned char* dst) {
+    constexpr int kChunks = DP / 8;
+    const int lane = threadIdx.x & 31;
+#pragma unroll 8
+    for (int i = lane; i < n * kChunks; i += 32) {
+      const int r = i / kChunks, c = i % kChunks;
+      const uint4* p = reinterpret_cast<const uint4*>(__shfl_sync(0xffffffffu, src, r));
+      *reinterpret_cast<uint4*>(dst + r * kStride + c * 16) = load(p + c, p && c * 8 < a.dim);
+    }
+  }
+  // kRows rows of the unit, from row r0 on (token, head of the group), by a warp.
+  __device__ void rows_again(int r0) {
+    const int lane = threadIdx.x & 31, col = lane * kCols;
+    // This warp's place in what held the tiles: the rows' queries, then 32 K rows.
+    unsigned char* scratch = reinterpret_cast<unsigned char*>(sh) - Tile<DP>::kSmemTiles +
+                             (threadIdx.x >> 5) * ((kRows + 32) * kStride);
+    int seen[kRows], most = 0;
+    long long out[kRows];  // bytes into out
+    unsigned long long q = 0;
+    float o[kRows][kCols];
+    uint32_t bad = 0, sums = 0;  // by bit: this lane's columns of all rows
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int r = min(r0 + k, x.ntok * a.group - 1), t = (int)a.by_group((uint32_t)r);
+      const long long at = x.s.row0 + x.tok0 + t;
+      const long long head = (long long)(x.h * a.group + r - t * a.group) * a.dim * 2;
+      seen[k] = max(0, x.s.len - x.s.n + x.tok0 + t + 1);
+      if (lane == k) q = (unsigned long long)(a.q + at * a.ld_q + head);
+      out[k] = at * a.ld_out + head;
+      uint32_t formed = 0;
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) {
+        const bool behind = last()[col + i] >= seen[k], nan = first(0)[col + i] < seen[k],
+                   pos = first(1)[col + i] < seen[k], neg = first(2)[col + i] < seen[k];
+        const bool sum = behind && !(nan || pos || neg);
+        bad |= (uint32_t)(behind && r0 + k == r) << (k * kCols + i);
+        formed |= (uint32_t)sum << (k * kCols + i);
+        o[k][i] = nan || (pos && neg) ? NAN : pos ? INFINITY : neg ? -INFINITY : 0.0f;
+      }
+      sums |= formed;
+      if (!__any_sync(0xffffffffu, formed)) seen[k] = 0;
+      most = max(most, seen[k]);
+    }
+    if (!__any_sync(0xffffffffu, bad)) return;
+    __syncwarp();
+    copy<kRows>(q, scratch);
+    float top[kRows], l[kRows], acc[kRows][kCols];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      top[k] = -INFINITY;
+      l[k] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) acc[k][i] = 0.0f;
+    }
+#pragma unroll 1
+    for (int key0 = 0; key0 < most; key0 += 32) {
+      const int key = key0 + lane;
+      unsigned long long kp = 0, vp = 0;
+      if (key < most) {
+        kp = (unsigned long long)row(0, key);
+        vp = (unsigned long long)row(1, key);
+      }
+      const bool there = vp != 0;
+      if (!there) vp = (unsigned long long)a.v;  // any rows, with weights of 0
+      __syncwarp();
+      copy<32>(kp, scratch + kRows * kStride);
+      __syncwarp();
+      float w[kRows];
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) w[k] = 0.0f;
+#pragma unroll 2
+      for (int c = 0; c < DP / 8; ++c) {
+        const uint4 z =
+            *reinterpret_cast<const uint4*>(scratch + (kRows + lane) * kStride + c * 16);
+        const uint32_t zw[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+          const uint4 u = *reinterpret_cast<const uint4*>(scratch + k * kStride + c * 16);
+          const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = Pack<T>::both(uw[i]), g = Pack<T>::both(zw[i]);
+            w[k] = fmaf(f.x, g.x, fmaf(f.y, g.y, w[k]));
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        const float s = key < seen[k] ? w[k] * a.scale_log2 : -INFINITY;
+        float m = s;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        m = fmaxf(m, top[k]);
+        const float f = weight(top[k], m);
+        top[k] = m;
+        w[k] = key < seen[k] ? ex2(s - (m == -INFINITY ? 0.0f : m)) : 0.0f;
+        l[k] = l[k] * f + w[k];
+        if (!there) w[k] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) acc[k][i] *= f;
+      }
+#pragma unroll 8
+      for (int j = 0; j < 32; ++j) {
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(__shfl_sync(0xffffffffu, vp, j));
+        float y[kCols];
+#pragma unroll
+        for (int i = 0; i < kCols; i += 2) {
+          const float2 f = Pack<T>::both(p[(min(col, a.dim - kCols) + i) / 2]);
+          y[i] = f.x;
+          y[i + 1] = f.y;
+        }
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+          const float wj = __shfl_sync(0xffffffffu, w[k], j);
+#pragma unroll
+          for (int i = 0; i < kCols; ++i)  // what it does not see may not be finite
+            acc[k][i] = wj == 0.0f ? acc[k][i] : fmaf(wj, y[i], acc[k][i]);
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+#pragma unroll
+      for (int d = 16; d; d >>= 1) l[k] += __shfl_xor_sync(0xffffffffu, l[k], d);
+      const float inv = l[k] > 0.0f || l[k] != l[k] ? 1.0f / l[k] : 0.0f;
+      T* d = reinterpret_cast<T*>(a.out + out[k]) + col;
+#pragma unroll
+      for (int i = 0; i < kCols; ++i)
+        if (bad >> (k * kCols + i) & 1)
+          d[i] = T(sums >> (k * kCols + i) & 1 ? acc[k][i] * inv : o[k][i]);
+    }
+  }
+  // The rows of one unit, by 256 threads.
+  __device__ void unit() {
+    const int common = max(0, x.s.len - x.s.n + x.tok0 + 1);  // keys that all rows see
+    barrier();
+    for (int i = threadIdx.x; i < 512; i += 256) first(0)[i] = i < 384 ? INT32_MAX : -1;
+    barrier();
+    look(common, min(x.s.len, x.nt * kTileKeys), false);
+    barrier();
+    int most = -1;
+    for (int i = 0; i < DP; ++i) most = max(most, last()[i]);
+    if (most < 0) return;
+    look(0, common, true);
+    barrier();
+#pragma unroll 1
+    for (int r = (threadIdx.x >> 5) * kRows; r < x.ntok * a.group; r += 8 * kRows) rows_again(r);
+  }
+};
 // What may be left at a CTA's end, by its softmax warps: the counts of a call whose waits
 // ran out, else the rows to be formed again, of the units whose output the CTA wrote.
-template <typename T>
+template <typename T, int DP>
 __device__ __noinline__ void finish(const AttendArgs& a, Shared* sh) {
   if (sh->failed) {
     if (threadIdx.x == 0) count_rest(a, sh);
     return;
   }
   Cursor cur = cursor(a, sh);
-  AttendPiece x;
-  while (cur.next(&x)) {
-    const bool whole = x.t0 == 0 && x.t1 == x.nt;
-    if (x.nt == 0 || !(whole || (sh->joined & (x.t0 > 0 ? 1 : 2)))) continue;
-    const int t = (int)a.by_group(threadIdx.x);
-    if (t < x.ntok) redo_row<T>(a, x, x.tok0 + t, threadIdx.x - t * a.group);
+  Redo<T, DP> r{a, sh};
+  while (cur.next(&r.x)) {
+    const bool whole = r.x.t0 == 0 && r.x.t1 == r.x.nt;
+    if (r.x.nt && (whole || (sh->joined & (r.x.t0 > 0 ? 1 : 2)))) r.unit();
   }
 }
 
@@ -1301,7 +1422,8 @@ struct Softmax {
           f1 *= inv;
         }
         if (whole) {
-          write_rows(p, base, from, to, tmem + 256 + (two ? w * DP : from), has0, f0, has1, f1, valid);
+          write_rows(p, base, from, to, tmem + 256 + (two ? w * DP : from), has0, f0, has1, f1,
+                     valid);
         } else {
 #pragma unroll 1
           for (int c = from; c < to; c += 32) {
@@ -1517,7 +1639,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     tmem_dealloc(tmem, kTmemCols);
   }
   // By softmax warps, whose registers suffice for any call.
-  if (warp < 8 && (sh->failed | sh->odd)) finish<T>(a, sh);
+  if (warp < 8 && (sh->failed | sh->odd)) finish<T, DP>(a, sh);
 }
 
 template <typename T, int DP>

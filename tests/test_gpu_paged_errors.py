@@ -311,3 +311,31 @@ def test_the_cache_calls_captured_and_replayed(T):
     for t, was in zip((tables, lens, top, pool), before):
         assert torch.equal(t, was)
     assert int(st) == capi.SPEC_ENOBLOCKS
+
+
+def test_rows_before_a_nan_beside_a_bad_table_entry():
+    """The positions of a bad entry stand for rows of zeros in the columns that are
+    formed again, too."""
+    capi = _capi()
+    n, D, bs, B = 300, 64, 16, 60
+    k, v = (rand((304, 1, D), torch.bfloat16, s) for s in (70, 71))
+    v[250, 0, 5:9] = float("nan")
+    q = rand((n, 4, D), torch.bfloat16, 72, 2.0)
+    pool = torch.stack([k, v]).view(2, 19, 1, bs, 1, D).permute(1, 2, 0, 3, 4, 5)
+    tables = torch.arange(19, dtype=torch.int32)
+    tables[3] = 19
+    st, ws = _status(), capi.attend_workspace(D)
+    every = q.repeat(B, 1, 1).cuda()
+    out, lse = torch.zeros_like(every), torch.zeros((B * n, 4), device="cuda")
+    capi.spec_attend_paged(every, pool.contiguous().cuda(), 0, tables.repeat(B, 1).cuda(),
+                           torch.full((B,), n, dtype=torch.int32).cuda(), out, st, ws, lse=lse)
+    torch.cuda.synchronize()
+    assert int(st) == capi.SPEC_EDEVICE
+    k[48:64], v[48:64] = 0.0, 0.0
+    with np.errstate(invalid="ignore"):
+        want = attend_rows(f64(q), f64(k[:n]), f64(v[:n]), D ** -0.5)
+    w = AttendResult(want.out[:250], want.lse[:250], want.mass[:250], want.vsum[:250],
+                     want.qk[:250])
+    for got, z in zip(out.view(B, n, 4, D).cpu(), lse.view(B, n, 4).cpu()):
+        check(got[:250], z[:250], w, torch.bfloat16, D)
+        assert got[250:, :, 5:9].isnan().all() and got[250:, :, :5].isfinite().all()
