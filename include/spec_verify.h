@@ -271,6 +271,7 @@ int spec_commit_paged(int B, int block_size, int max_blocks,
  *         is the slot block * block_size + offset of the i-th new row of
  *         sequence b; entries from row_off[B] on are -1, so a captured graph
  *         may use one capacity for batches of any size.
+ * B = 0 returns at once and writes nothing, row_off and slot_map included.
  * Every check (lengths and counts not negative, new lengths within the table,
  * the entry of a part-filled last block and popped ids inside
  * [0, num_blocks), the stack's height, row_off[B] <= capacity) is made before
@@ -295,11 +296,12 @@ int spec_extend_paged(int B, int block_size, int max_blocks, int32_t* block_tabl
  *            boundaries; kv_heads * head_dim * 2 is a multiple of 16.
  * slot_map : int64 [T], as written by spec_extend_paged; rows with slot -1 are
  *            skipped. Any other slot outside [0, num_blocks * block_size)
- *            records SPEC_EINVAL and its row is skipped. Of rows that name the
- *            same slot any one may end up there, or parts of several.
+ *            records SPEC_EINVAL and its row is skipped; the others are stored.
+ *            Of rows that name the same slot any one may end up there, or parts of
+ *            several.
  * kv_pool  : [num_blocks, layers, 2, block_size, kv_heads, head_dim], as for
  *            spec_commit_paged; `layer` is the layer written.
- * Does nothing while *dev_status (may be NULL) holds an error.
+ * Does nothing if *dev_status (may be NULL) held an error before the call.
  * ------------------------------------------------------------------------- */
 int spec_store_kv(const void* k, int64_t ld_k, const void* v, int64_t ld_v, int T,
                   const int64_t* slot_map, void* kv_pool, int num_blocks, int layers, int layer,
@@ -316,7 +318,8 @@ int spec_store_kv(const void* k, int64_t ld_k, const void* v, int64_t ld_v, int 
  * query head h with K/V head h / (q_heads / kv_heads).
  *
  * q, out : [T, q_heads, head_dim], k, v : [T, kv_heads, head_dim], heads
- *          contiguous, row t at element t * ld; 16-byte boundaries.
+ *          contiguous, row t at element t * ld; 16-byte boundaries. out and lse
+ *          overlap no input.
  * dtype  : SPEC_BF16 or SPEC_F16 (all four). Products and sums are taken in
  *          float32; the softmax weights are rounded to dtype for the product
  *          with v.
@@ -330,6 +333,8 @@ int spec_store_kv(const void* k, int64_t ld_k, const void* v, int64_t ld_v, int 
  *          sum_j exp(scale * q_i . k_j).
  * dev_status : may be NULL. SPEC_ETIMEOUT if a bounded wait ran out: outputs
  *          are then not to be used, which a caller without it cannot tell.
+ *          Attention is formed whatever it holds before the call, also an error
+ *          of tables that did not grow.
  * ws     : spec_attend_workspace_bytes(head_dim) bytes, 256-byte aligned, set to
  *          zero before its first use; every call, one whose wait ran out among
  *          them, leaves it ready for the next, also of another head_dim that it
@@ -364,7 +369,11 @@ int spec_attend_prompt(const void* q, int64_t ld_q, const void* k, int64_t ld_k,
  *          them): row i of n sees positions 0 .. seq_lens-n+i. Else the
  *          staging buffer of spec_commit_paged, [B, Kp1, layers, 2, kv_heads,
  *          head_dim]: row i sees all seq_lens cached positions, then the
- *          staged rows 0..i (n <= Kp1).
+ *          staged rows 0..i (n <= Kp1). The call's rows are the first staged
+ *          ones: the rows of a check. A row drafted after others that are staged
+ *          already cannot attend them in a call of its own; such a call has
+ *          them again, or they are in the cache.
+ * Pages whose rows are no multiple of 8 take about five times as long as others.
  * A row that sees nothing gets out = 0 and lse = -infinity.
  * A sequence with seq_lens negative or beyond the table, or more than Kp1 rows
  * beside a staging buffer, sees nothing; a table entry outside

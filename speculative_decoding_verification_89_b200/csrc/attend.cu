@@ -26,13 +26,15 @@
 // reads as its left operand for O += P~ V. While one warpgroup works on its
 // scores, the tensor cores form the other's.
 //
-// Times on the device, 32 query and 8 K/V heads of 128, bf16. 8192 rows: 472 us,
-// 1165 TFLOP/s (332 us at the measured 1656): a K/V tile with two query tiles takes
+// Times on the device, 32 query and 8 K/V heads of 128, bf16, of calls a few at a time; in
+// brackets in a loop of calls for seconds, where power holds the clock down. 8192 rows:
+// 472 us (555), 1165 TFLOP/s (332 us at the measured 1656): a K/V tile with two query tiles takes
 // about 3500 cycles where the products alone need 2048 and the exponentials, 16 a
 // cycle, 2048; maximum, scaling, rounding and the hand-over between the two make
-// up the rest. 64 sequences of 9 staged rows over 512 to 4096 keys 118 us, one
-// row over 65000 keys 54 us: 4.9 TB/s both (89 and 41 us at the measured 6.55
-// TB/s), bound by HBM and the gaps between units. One row over 700 keys 12.5 us:
+// up the rest. 64 sequences of 9 staged rows over 512 to 4096 keys 114 to 129 us by the
+// card (137), one row over 65000 keys 53 to 57 (57): 4.5 to 5.1 TB/s both (89 and 41 us
+// at the measured 6.55 TB/s), bound by HBM and the gaps between units. 8192 rows of
+// heads of 64: 415 us, bound by exponentials alone. One row over 700 keys 13 us:
 // launch, plan, first instruction fetches and join, one after the other.
 #include <cuda_fp16.h>
 
@@ -1601,8 +1603,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   find_run(a, sh);  // its barriers publish the above
   tc_fence_after();
   const uint32_t tiles = smem_u32(smem), tmem = sh->tmem;
-  // Of the 384 * 168 registers of the launch, 208 to each of the 256 softmax threads
-  // (a row's 128 scores and their weights stay in registers), 88 to the 128 others.
+  // Of the 384 * 168 registers of the launch, 208 to each of the 256 softmax threads, for a
+  // row's 128 scores and their weights, 88 to the 128 others. (80 to 88 bytes a thread
+  // are spilled, as the compiler reports.)
   bool ok = true;
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");

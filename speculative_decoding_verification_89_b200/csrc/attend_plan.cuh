@@ -32,10 +32,10 @@ namespace specv {
 constexpr int kTileRows = 128;  // query rows of a tile
 constexpr int kTileKeys = 128;  // keys of a K/V tile
 // A unit's fixed cost, in K/V tiles: what its first loads, the filling of the
-// pipeline and its output take. Measured with 2, 3, 4: 8192 rows 467, 470, 473 us;
-// 16 ragged prompts 335, 342, 353; one row over 65000 keys 56, 55, 54; 64 x 9 rows
-// over a cache 119, 119, 121. (Before the two tiles of a unit were kept out of step, 1
-// cost 559 us for 8192 rows where 3 took 490.)
+// pipeline and its output take. Measured with 2, 3, 4: 8192 rows 462, 466, 471 us;
+// 16 ragged prompts 345, 348, 358; four chunks 175 each; one row over 65000 keys 56, 54,
+// 53. So long prompts would gain 1 % with 2, and a step of decoding over a long cache
+// lose 4 %.
 constexpr int kUnitCost = 3;
 
 // sum_{i=0}^{n-1} floor((a*i + b) / m) for n, a, b >= 0, m > 0: the lattice

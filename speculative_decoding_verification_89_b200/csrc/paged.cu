@@ -347,10 +347,11 @@ __global__ void __launch_bounds__(kStoreThreads) store_flag_kernel(StoreArgs a) 
 }  // namespace
 
 // One launch for up to kClusterRows rows of slot map (a cluster of 8 CTAs, one CTA
-// for up to kOneCtaRows): a sequence growing by a row takes 4.6 us, 256 growing by
-// up to 5 rows 6.2 us, as long as a plan and a second launch that fills the map,
-// but a launch less for the host. Else the two launches: a cluster's few SMs
-// would take longer (64 prompts of up to 4096 rows: 24 us against 11.7).
+// for up to kOneCtaRows), else a plan and a second launch that fills the map. 64
+// sequences growing to rows in all, one launch against two: 1024 5.8 and 6.9 us, 4096
+// 5.9 and 6.9, 8192 6.9 and 6.7, 16384 7.9 and 7.0, 147200 25.5 and 10.3, as a cluster
+// has few SMs; 4096 sequences growing by a row 19.8 and 31.4. One CTA against eight:
+// 512 rows 5.7 and 5.5, 1024 7.0 and 5.8.
 constexpr long long kClusterRows = 8192, kOneCtaRows = 512;
 constexpr int kClusterSeqs = 4096;  // whose records fit the cluster's shared memory
 
