@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kFillThreads) extend_fill_kernel(ExtendArgs a)
 // K and V rows to their slots: a warp per token, up to four 16-byte vectors of
 // each row per lane in flight before the first is stored, loaded while the slot
 // is looked up. Bound by HBM (each byte read and written once): 20000 rows of 8
-// heads of 128 take 27.4 us, 6.0 TB/s (25.0 us at the measured copy rate); 64 rows
+// heads of 128 take 28.5 us, 5.8 TB/s (25.0 us at the measured copy rate); 64 rows
 // 2.3 us, one warp's chain of two loads and a store, then the cluster's barrier.
 constexpr int kStoreThreads = 256;
 constexpr int kStoreRows = kStoreThreads / 32;  // rows of a CTA
@@ -318,7 +318,7 @@ __device__ __forceinline__ bool store_row(const StoreArgs& a, int t) {
 // call's own error, of a bad slot, may appear there only once every row has read
 // the word: after the barrier of the cluster that is the whole grid (up to
 // kStoreClusterRows rows), else in a launch of its own (store_flag_kernel). 64 rows
-// take 2.3 us with the barrier, 2.5 with the launch, and from Python, where the
+// take 2.3 us with the barrier, 3.0 with the launch, and from Python, where the
 // host is the limit, 7.1 and 8.9.
 template <bool kCluster>
 __global__ void __launch_bounds__(kStoreThreads) store_kv_kernel(StoreArgs a) {
@@ -332,15 +332,13 @@ __global__ void __launch_bounds__(kStoreThreads) store_kv_kernel(StoreArgs a) {
   }
 }
 
-// Flags bad slots after store_kv_kernel, whose CTAs have waited for all work before
-// them when they let this launch begin: the map is complete, and is read while
-// the last rows are stored.
+// Flags bad slots after store_kv_kernel.
 __global__ void __launch_bounds__(kStoreThreads) store_flag_kernel(StoreArgs a) {
+  pdl_begin();  // every row has read the status word
   bool bad = false;
   for (long long t = (long long)blockIdx.x * blockDim.x + threadIdx.x; t < a.T;
        t += (long long)gridDim.x * blockDim.x)
     bad |= bad_slot(a, a.slot_map[t]);
-  pdl_begin();  // every row has read the status word
   if (bad) set_status(a.status, SPEC_EINVAL);
 }
 
