@@ -911,7 +911,7 @@ __device__ __forceinline__ float weight(float m, float ref) {
 // forms four rows at once, a key per lane: 8192 rows with one NaN near their end take
 // 40 ms (350 with a thread per row), with all values infinite 2.5 (122).
 // (Values taken out of the tiles that not all rows of a unit see, before their
-// products, cost 16 ragged prompts 30 us; looking at the outputs costs 10.)
+// products, cost 16 ragged prompts 30 us; looking at the outputs costs 10 to 14.)
 template <typename T, int DP>
 struct Redo {
   static constexpr int kCols = DP / 32;  // columns of a lane
@@ -926,7 +926,10 @@ struct Redo {
   // infinity, a negative one; the last with any of them that not all rows see.
   __device__ int* first(int kind) const { return reinterpret_cast<int*>(sh->ml) + kind * 128; }
   __device__ int* last() const { return first(3); }
-  __device__ void barrier() const { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+  __device__ void barrier() const {
+    __syncwarp();  // the barrier takes whole warps
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+  }
   // K (v = 0) or V row of a key; null: a bad table entry, which stands for zeros
   __device__ const unsigned char* row(int v, int key) const {
     const int pooled = a.stage_k ? x.s.len - x.s.n : x.s.len;

@@ -326,6 +326,7 @@ __global__ void __launch_bounds__(kStoreThreads) store_kv_kernel(StoreArgs a) {
   const int t = blockIdx.x * kStoreRows + (threadIdx.x >> 5);
   const bool bad = t < a.T && store_row(a, t);
   if constexpr (kCluster) {
+    __syncwarp();  // the barrier takes whole warps
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (bad && (threadIdx.x & 31) == 0) set_status(a.status, SPEC_EINVAL);
